@@ -13,6 +13,13 @@ kernels.  The functions carry the C ABI's names (see ``include/fcm.h``):
     fcm_dw_fwd / fcm_pw_fwd / fcm_conv_fwd / fcm_pwdwpw_lbl   (layer-by-layer baselines)
     fcm_pwdwpw_lbl_noalloc   (the three-layer baseline with the library's static scratch)
 
+and the sequence operators, each on its own small problem descriptor:
+
+    fcm_dw1d_fwd / fcm_dw1d_step(dw1d_problem(...), x, w, bias, ...)   causal depthwise layer
+    fcm_scan_fwd / fcm_scan_step(scan_problem(...), x, dt, A, Bm, Cm, ...)   selective scan
+    fcm_q4_fwd(q4_problem(...), x, q, scales, zeros, bias, y)   4-bit pointwise layer
+    fcm_beam_select / fcm_beam_reorder(beam_problem(...), ...)   beam search
+
 Tensor arguments are torch tensors on the GPU (or raw integer device addresses, or
 None where the ABI allows NULL); PyTorch only provides device memory and the stream
 (``torch.cuda.current_stream()`` unless one is passed).  A non-OK status raises
@@ -101,8 +108,34 @@ class fcm_chain_group(ctypes.Structure):
                 ("gma", _f64)]
 
 
+class fcm_dw1d_problem(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("dtype", "D", "W", "tokens", "seqs", "slots", "silu")] + \
+               [(n, _i64) for n in ("ldx", "ldy")]
+
+
+class fcm_scan_problem(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("dtype", "D", "N", "groups", "tokens", "seqs", "slots",
+                                    "softplus")] + \
+               [(n, _i64) for n in ("ldx", "lddt", "ldb", "ldc", "ldz", "ldy")]
+
+
+class fcm_q4_problem(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("dtype", "M", "C", "K", "group", "act")] + \
+               [(n, _i64) for n in ("ldx", "ldy")]
+
+
+class fcm_beam_problem(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("dtype", "requests", "beams", "vocab", "eos")] + \
+               [("ldl", _i64)]
+
+
+FCM_BEAM_POOLS = 8
+
 # every symbol include/fcm.h declares
-EXPORTS = ("fcm_default_device_spec", "fcm_query_device_spec", "fcm_plan", "fcm_plan_variant",
+EXPORTS = ("fcm_dw1d_fwd", "fcm_dw1d_step", "fcm_scan_workspace", "fcm_scan_fwd",
+           "fcm_scan_step", "fcm_q4_fwd", "fcm_beam_workspace", "fcm_beam_select",
+           "fcm_beam_reorder",
+           "fcm_default_device_spec", "fcm_query_device_spec", "fcm_plan", "fcm_plan_variant",
            "fcm_plan_chain",
            "fcm_num_variants", "fcm_variant_name", "fcm_pack_weights", "fcm_dwpw_fwd",
            "fcm_tune",
@@ -160,6 +193,18 @@ def lib() -> ctypes.CDLL:
             L.fcm_dw_fwd.argtypes = [P(fcm_plan_t), vp, vp, fp, fp, vp, vp]
             L.fcm_pw_fwd.argtypes = [P(fcm_plan_t), vp, vp, fp, fp, vp, vp]
             L.fcm_conv_fwd.argtypes = [P(fcm_plan_t), vp, vp, fp, fp, vp, vp]
+            L.fcm_dw1d_fwd.argtypes = [P(fcm_dw1d_problem)] + [vp] * 9
+            L.fcm_dw1d_step.argtypes = [P(fcm_dw1d_problem)] + [vp] * 7
+            L.fcm_scan_workspace.argtypes = [P(fcm_scan_problem)]
+            L.fcm_scan_workspace.restype = _i64
+            L.fcm_scan_fwd.argtypes = [P(fcm_scan_problem)] + [vp] * 15
+            L.fcm_scan_step.argtypes = [P(fcm_scan_problem)] + [vp] * 12
+            L.fcm_q4_fwd.argtypes = [P(fcm_q4_problem)] + [vp] * 7
+            L.fcm_beam_workspace.argtypes = [P(fcm_beam_problem)]
+            L.fcm_beam_workspace.restype = _i64
+            L.fcm_beam_select.argtypes = [P(fcm_beam_problem)] + [vp] * 9
+            L.fcm_beam_reorder.argtypes = [P(fcm_beam_problem), vp, vp, vp, _i32, P(vp),
+                                           P(_i64), P(_i64), vp]
             L.fcm_status_str.restype = ctypes.c_char_p
             L.fcm_status_str.argtypes = [ctypes.c_int]
             L.fcm_last_error.restype = ctypes.c_char_p
@@ -168,7 +213,9 @@ def lib() -> ctypes.CDLL:
                          "fcm_plan_variant", "fcm_pack_weights", "fcm_dwpw_fwd",
                          "fcm_b2b_conv_fwd", "fcm_pwdw_fwd", "fcm_pwpw_fwd", "fcm_dw_fwd",
                          "fcm_pw_fwd", "fcm_conv_fwd", "fcm_pwdwpw_fwd", "fcm_pwdwpw_lbl",
-                         "fcm_pwdwpw_lbl_noalloc", "fcm_tune_pwdwpw", "fcm_tune"):
+                         "fcm_pwdwpw_lbl_noalloc", "fcm_tune_pwdwpw", "fcm_tune", "fcm_dw1d_fwd",
+                         "fcm_dw1d_step", "fcm_scan_fwd", "fcm_scan_step", "fcm_q4_fwd",
+                         "fcm_beam_select", "fcm_beam_reorder"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -401,3 +448,98 @@ def fcm_pw_fwd(plan, t, w_pw, scale2, bias2, y, stream=None):
 def fcm_conv_fwd(plan, x, w1, scale1, bias1, t, stream=None):
     _check(lib().fcm_conv_fwd(ctypes.byref(plan), _ptr(x), _ptr(w1), _ptr(scale1),
                               _ptr(bias1), _ptr(t), _stream(stream)), "fcm_conv_fwd")
+
+
+# ------------------------------------------------------------------------------------
+# sequence operators
+# ------------------------------------------------------------------------------------
+def _code(dtype):
+    return DTYPE_CODES[dtype] if isinstance(dtype, str) else dtype
+
+
+def dw1d_problem(dtype="f16", D=8, W=4, tokens=1, seqs=1, slots=0, silu=True, ldx=0,
+                 ldy=0) -> fcm_dw1d_problem:
+    """Causal depthwise layer of W taps over D channels: `tokens` rows that belong to `seqs`
+    sequences, whose windows live in `slots` slots.  Row strides in elements; 0: dense."""
+    return fcm_dw1d_problem(_code(dtype), D, W, tokens, seqs, slots, int(bool(silu)), ldx, ldy)
+
+
+def scan_problem(dtype="f16", D=8, N=16, groups=1, tokens=1, seqs=1, slots=0, softplus=True,
+                 ldx=0, lddt=0, ldb=0, ldc=0, ldz=0, ldy=0) -> fcm_scan_problem:
+    """Selective scan of D channels with N states each; the channels of one of `groups` groups
+    share their B and C rows.  Row strides in elements; 0: dense."""
+    return fcm_scan_problem(_code(dtype), D, N, groups, tokens, seqs, slots,
+                            int(bool(softplus)), ldx, lddt, ldb, ldc, ldz, ldy)
+
+
+def q4_problem(dtype="f16", M=1, C=8, K=8, group=128, act="none", ldx=0,
+               ldy=0) -> fcm_q4_problem:
+    """Pointwise layer C -> K with 4-bit weights, `group` channels to a scale, for M tokens."""
+    return fcm_q4_problem(_code(dtype), M, C, K, group,
+                          ACT_CODES[act] if isinstance(act, str) else act, ldx, ldy)
+
+
+def beam_problem(dtype="f32", requests=1, beams=1, vocab=1, eos=-1, ldl=0) -> fcm_beam_problem:
+    """Beam search of `requests` requests with `beams` beams each over `vocab` tokens."""
+    return fcm_beam_problem(_code(dtype), requests, beams, vocab, eos, ldl)
+
+
+def fcm_dw1d_fwd(prob, x, w, bias, cu, slots, carry, state, y, stream=None):
+    _check(lib().fcm_dw1d_fwd(prob, _ptr(x), _ptr(w), _ptr(bias), _ptr(cu), _ptr(slots),
+                              _ptr(carry), _ptr(state), _ptr(y), _stream(stream)),
+           "fcm_dw1d_fwd")
+
+
+def fcm_dw1d_step(prob, x, w, bias, slots, state, y, stream=None):
+    _check(lib().fcm_dw1d_step(prob, _ptr(x), _ptr(w), _ptr(bias), _ptr(slots), _ptr(state),
+                               _ptr(y), _stream(stream)), "fcm_dw1d_step")
+
+
+def fcm_scan_workspace(prob) -> int:
+    n = lib().fcm_scan_workspace(prob)
+    if n < 0:
+        _check(FCM_ERR_INVALID_ARG, "fcm_scan_workspace")
+    return n
+
+
+def fcm_scan_fwd(prob, x, dt, A, Bm, Cm, skip, dt_bias, z, cu, slots, carry, state, workspace, y,
+                 stream=None):
+    _check(lib().fcm_scan_fwd(prob, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(skip),
+                              _ptr(dt_bias), _ptr(z), _ptr(cu), _ptr(slots), _ptr(carry),
+                              _ptr(state), _ptr(workspace), _ptr(y), _stream(stream)),
+           "fcm_scan_fwd")
+
+
+def fcm_scan_step(prob, x, dt, A, Bm, Cm, skip, dt_bias, z, slots, state, y, stream=None):
+    _check(lib().fcm_scan_step(prob, _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(skip),
+                               _ptr(dt_bias), _ptr(z), _ptr(slots), _ptr(state), _ptr(y),
+                               _stream(stream)), "fcm_scan_step")
+
+
+def fcm_q4_fwd(prob, x, q, scales, zeros, bias, y, stream=None):
+    _check(lib().fcm_q4_fwd(prob, _ptr(x), _ptr(q), _ptr(scales), _ptr(zeros), _ptr(bias),
+                            _ptr(y), _stream(stream)), "fcm_q4_fwd")
+
+
+def fcm_beam_workspace(prob) -> int:
+    n = lib().fcm_beam_workspace(prob)
+    if n < 0:
+        _check(FCM_ERR_INVALID_ARG, "fcm_beam_workspace")
+    return n
+
+
+def fcm_beam_select(prob, logits, scores, done, workspace, next_scores, parent, token,
+                    next_done, stream=None):
+    _check(lib().fcm_beam_select(prob, _ptr(logits), _ptr(scores), _ptr(done), _ptr(workspace),
+                                 _ptr(next_scores), _ptr(parent), _ptr(token), _ptr(next_done),
+                                 _stream(stream)), "fcm_beam_select")
+
+
+def fcm_beam_reorder(prob, parent, slots, next_slots, pools, stream=None):
+    """pools: state tensors whose first axis counts slots (contiguous)."""
+    n = len(pools)
+    ptrs = (ctypes.c_void_p * n)(*[_ptr(t) for t in pools])
+    bytes_ = (_i64 * n)(*[t.stride(0) * t.element_size() for t in pools])
+    slots_ = (_i64 * n)(*[t.shape[0] for t in pools])
+    _check(lib().fcm_beam_reorder(prob, _ptr(parent), _ptr(slots), _ptr(next_slots), n, ptrs,
+                                  bytes_, slots_, _stream(stream)), "fcm_beam_reorder")

@@ -38,7 +38,12 @@ SOURCES = [
     ("kernels/dwpw_gen.hip", True),
     ("kernels/lbl.hip", True),
     ("kernels/b2b.hip", True),
+    ("kernels/dw1d.hip", True),
+    ("kernels/scan.hip", True),
+    ("kernels/q4.hip", True),
+    ("kernels/beam.hip", True),
     ("api.cpp", True),
+    ("api_seq.cpp", True),
     ("plan.cpp", False),
 ]
 

@@ -17,6 +17,7 @@
 #include "launchers.h"
 #include "lbl_tiles.h"
 #include "plan.h"
+#include "seq.h"
 
 namespace fcm {
 namespace {
@@ -296,6 +297,18 @@ fcm_status tune_impl(const fcm_problem* prob, const fcm_device_spec* spec, int32
     return ok();
 }
 }  // namespace
+
+fcm_status set_error(fcm_status s, const char* text) noexcept {
+    try {
+        if (text)
+            g_last_error = text;
+        else
+            g_last_error.clear();
+    } catch (...) {
+        // out of memory for the text: the status still says what happened
+    }
+    return s;
+}
 }  // namespace fcm
 
 using namespace fcm;

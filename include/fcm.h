@@ -407,6 +407,153 @@ fcm_status fcm_pw_fwd(const fcm_plan_t* plan, const void* t, const void* w_pw,
 fcm_status fcm_conv_fwd(const fcm_plan_t* plan, const void* x, const void* w1,
                         const float* scale1, const float* bias1, void* t, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Sequence operators: the layers of a state-space sequence model, whose blocks are
+ * pointwise and depthwise layers along one axis, for prompts and for single tokens.
+ *
+ * A batch of prompts is packed along one token axis: sequence b owns rows cu[b] ..
+ * cu[b+1]-1 of every [tokens][...] tensor, with cu an int32 array of seqs+1
+ * non-decreasing offsets in device memory (cu[0] = 0, cu[seqs] = tokens; a sequence may
+ * be empty).  Offsets are clamped to [0, tokens] on the device; rows that belong to no
+ * sequence are left unwritten.  What a sequence carries from one call to the next lives
+ * in a slot of a state array: slots[b] is sequence b's slot (int32, NULL: slot b), and
+ * no two sequences of a call may share one.  A value outside [0, slots) names no slot:
+ * a prompt then starts from zero and stores nothing; a row of a single-token call is
+ * idle (its output is zero, no state is read or written).  carry[b] (int32) != 0: the
+ * prompt continues from its slot's state; 0, or carry == NULL: it starts from zero.
+ * Row strides (ld*) are in elements; the last axis is contiguous; 0 means densely
+ * packed.  Tensor pointers need the alignment of their element only, except where a
+ * call says otherwise; rows and pointers that are 16-byte aligned take the wide loads.
+ * Inputs and outputs must not overlap.  Sums, the recurrence and its state are fp32.
+ * The calls are asynchronous on `stream`, allocate nothing and can be captured.
+ * Errors: INVALID_ARG (NULL or misaligned pointer, bad size, a row stride below the
+ * row), UNSUPPORTED (a type or size without a kernel), HIP (launch failure).
+ * --------------------------------------------------------------------------------- */
+
+/* Causal depthwise layer along the token axis (a depthwise 1-D convolution of W taps):
+ *   y[t][d] = act(bias[d] + sum_k w[d][k] * x[t - (W-1) + k][d])
+ * where rows before a sequence's start are its carried window or zero. */
+typedef struct {
+    int32_t dtype;   /* FCM_F32, FCM_F16 or FCM_BF16: x, w, state, y */
+    int32_t D, W;    /* channels; taps, 2 to 8 */
+    int32_t tokens;  /* rows of x and y */
+    int32_t seqs;    /* sequences (single-token call: must equal tokens) */
+    int32_t slots;   /* slots of the state array */
+    int32_t silu;    /* 1: act(v) = v * sigmoid(v); 0: none */
+    int64_t ldx, ldy;
+} fcm_dw1d_problem;
+
+/* Prompts.  x: [tokens][D]; w: [D][W]; bias: [D] fp32 or NULL; state: [slots][W-1][D], the
+ * last W-1 inputs of each sequence, oldest first, read where carry says so and always
+ * written (NULL: nothing is carried or stored; slots and carry must be NULL too). */
+fcm_status fcm_dw1d_fwd(const fcm_dw1d_problem* prob, const void* x, const void* w,
+                        const float* bias, const int32_t* cu, const int32_t* slots,
+                        const int32_t* carry, void* state, void* y, void* stream);
+
+/* One token of each sequence: row b of x continues the sequence in slots[b]; its window is
+ * read and moved on in place. */
+fcm_status fcm_dw1d_step(const fcm_dw1d_problem* prob, const void* x, const void* w,
+                         const float* bias, const int32_t* slots, void* state, void* y,
+                         void* stream);
+
+/* Selective state-space scan, channel d and state n, group g = d / (D/groups):
+ *   delta = dt[t][d] + dt_bias[d], through softplus(v) = log(1 + exp(v)) if `softplus`
+ *   h[d][n] = exp(delta * A[d][n]) * h[d][n] + delta * Bm[t][g][n] * x[t][d]
+ *   y[t][d] = (sum_n Cm[t][g][n] * h[d][n] + skip[d] * x[t][d]) * (z ? z * sigmoid(z) : 1)
+ * A <= 0 keeps the recurrence bounded. */
+typedef struct {
+    int32_t dtype;    /* FCM_F32, FCM_F16 or FCM_BF16: x, dt, Bm, Cm, z, y */
+    int32_t D, N;     /* channels; states of a channel, 1 to 64 */
+    int32_t groups;   /* channel groups that share Bm and Cm rows; divides D (0: 1) */
+    int32_t tokens, seqs, slots; /* as for the depthwise layer */
+    int32_t softplus; /* 1: delta goes through softplus */
+    int64_t ldx, lddt, ldb, ldc, ldz, ldy;
+} fcm_scan_problem;
+
+/* Bytes of device memory fcm_scan_fwd needs for `prob` (0 if it needs none), or -1 if the
+ * problem is invalid.  Host only. */
+int64_t fcm_scan_workspace(const fcm_scan_problem* prob);
+
+/* Prompts.  x, dt, z: [tokens][D] (z may be NULL); A: [D][N] fp32; Bm, Cm:
+ * [tokens][groups][N]; skip, dt_bias: [D] fp32 or NULL; state: [slots][D][N] fp32, read
+ * where carry says so and always written (NULL as for fcm_dw1d_fwd); workspace: 16-byte
+ * aligned, fcm_scan_workspace(prob) bytes, whose contents need not be set and do not
+ * outlive the call. */
+fcm_status fcm_scan_fwd(const fcm_scan_problem* prob, const void* x, const void* dt,
+                        const float* A, const void* Bm, const void* Cm, const float* skip,
+                        const float* dt_bias, const void* z, const int32_t* cu,
+                        const int32_t* slots, const int32_t* carry, float* state,
+                        void* workspace, void* y, void* stream);
+
+/* One token of each sequence: the state in slots[b] is read and updated in place. */
+fcm_status fcm_scan_step(const fcm_scan_problem* prob, const void* x, const void* dt,
+                         const float* A, const void* Bm, const void* Cm, const float* skip,
+                         const float* dt_bias, const void* z, const int32_t* slots,
+                         float* state, void* y, void* stream);
+
+/* Pointwise layer with 4-bit weights for a few tokens:
+ *   y[m][k] = act(bias[k] + sum_c (q[k][c] - zeros[k][c/group]) * scales[k][c/group] * x[m][c])
+ * q: [K][C/2], two codes of 0..15 a byte, the even channel in the low half; scales:
+ * [K][ceil(C/group)] in the storage type; zeros: [K][ceil(C/group)] uint8 in 0..15, or NULL
+ * for 8 throughout (the low four bits are used); bias: [K] fp32 or NULL; x: [M][C];
+ * y: [M][K].  The last group may be short.  The arrays are read as they are: nothing is
+ * packed.  Products are exact and summed in fp32; only y is rounded. */
+typedef struct {
+    int32_t dtype;   /* FCM_F16 or FCM_BF16: x, scales, y */
+    int32_t M, C, K; /* tokens; input channels, a multiple of 8; output channels */
+    int32_t group;   /* 32, 64 or 128 channels share a scale */
+    int32_t act;     /* fcm_act */
+    int64_t ldx, ldy;
+} fcm_q4_problem;
+
+/* x needs 16-byte alignment and ldx a multiple of 8; q 4-byte alignment. */
+fcm_status fcm_q4_fwd(const fcm_q4_problem* prob, const void* x, const void* q,
+                      const void* scales, const uint8_t* zeros, const float* bias, void* y,
+                      void* stream);
+
+/* Beam search: the next beams of each request, and the states that go with them. */
+typedef struct {
+    int32_t dtype;    /* FCM_F32, FCM_F16 or FCM_BF16: logits */
+    int32_t requests; /* independent searches */
+    int32_t beams;    /* beams of a request, 1 to 32 */
+    int32_t vocab;
+    int32_t eos;      /* token that ends a beam; -1: none */
+    int64_t ldl;      /* row stride of the logits */
+} fcm_beam_problem;
+
+/* Bytes of device memory fcm_beam_select needs, or -1 if the problem is invalid. */
+int64_t fcm_beam_workspace(const fcm_beam_problem* prob);
+
+/* The `beams` best continuations of each request among beams * vocab, best first:
+ *   score(w, v) = scores[w] + logits[w][v] - log(sum_u exp(logits[w][u]))
+ * A beam with done[w] != 0 only continues with eos, at its own score.  Equal scores go to
+ * the lowest w * vocab + v.  -inf logits are masked tokens; NaN counts as -inf and +inf as
+ * the largest float; a row without any finite logit, or a beam whose score is -inf,
+ * continues at -inf.  logits: [requests*beams][vocab]; scores (fp32, not NaN), done (int32
+ * or NULL: none is done): [requests*beams].  Out, all [requests*beams]: next_scores fp32;
+ * parent, the beam of the same request it continues, and token, int32; next_done int32 or
+ * NULL (done, or token == eos).  workspace: 16-byte aligned, fcm_beam_workspace(prob)
+ * bytes. */
+fcm_status fcm_beam_select(const fcm_beam_problem* prob, const void* logits,
+                           const float* scores, const int32_t* done, void* workspace,
+                           float* next_scores, int32_t* parent, int32_t* token,
+                           int32_t* next_done, void* stream);
+
+/* Most state arrays one fcm_beam_reorder call takes. */
+#define FCM_BEAM_POOLS 8
+
+/* Gives the next beams their states: next_slots[i] becomes a slot holding the state of
+ * slots[parent of i].  Of the children of one beam the first keeps its slot; the others
+ * take, in order, the slots of the beams without a child, and only those are copied, in
+ * place: pool p is [..][pool_bytes[p]] with pool_slots[p] slots (pool_bytes a multiple of 4
+ * and the pools 4-byte aligned; multiples of 16 take the wide copies).  slots, next_slots:
+ * [requests*beams] int32, distinct arrays; the slots must be distinct.  A parent outside
+ * [0, beams) counts as beam 0; a slot outside a pool is not copied from or to. */
+fcm_status fcm_beam_reorder(const fcm_beam_problem* prob, const int32_t* parent,
+                            const int32_t* slots, int32_t* next_slots, int32_t npools,
+                            void* const* pools, const int64_t* pool_bytes,
+                            const int64_t* pool_slots, void* stream);
+
 /* Static description of a status code, and the calling thread's last error detail
  * (empty after a successful call). */
 const char* fcm_status_str(fcm_status s);
