@@ -113,6 +113,7 @@ fcm_status check_scan(const fcm_scan_problem* p) {
         return invalid("D and N must be positive, groups, tokens, seqs and slots not negative");
     if (p->D > (1 << 24)) return unsupported("D above 2^24");
     if (p->N > 64) return unsupported("more than 64 states of a channel");
+    if ((long long)p->seqs * p->D > (1 << 25)) return unsupported("seqs * D above 2^25");
     if (p->groups > 0 && p->D % p->groups != 0) return invalid("groups must divide D");
     if (p->softplus != 0 && p->softplus != 1) return invalid("softplus must be 0 or 1");
     if ((long long)p->tokens + p->seqs > (1 << 30)) return invalid("tokens + seqs is above 2^30");

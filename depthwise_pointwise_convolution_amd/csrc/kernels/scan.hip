@@ -9,53 +9,275 @@ namespace {
 
 constexpr float kLog2e = 1.44269504f;
 
-// One thread per (sequence, channel): the channel's N states in registers, token after token.
-template <typename T, int NP>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a, int cblocks, long long units) {
-    const T *x = (const T*)a.x, *dt = (const T*)a.dt, *z = (const T*)a.z;
-    const T *Bm = (const T*)a.Bm, *Cm = (const T*)a.Cm;
-    T* y = (T*)a.y;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-        const int seq = (int)(u / cblocks);
-        const int d = (int)(u % cblocks) * 64 + threadIdx.x;
-        if (d >= a.D) continue;
-        const int g = d / (a.D / a.groups);
-        const int start = seq_offset(a.cu, seq, a.tokens);
-        const int end = seq_offset(a.cu, seq + 1, a.tokens);
-        const int slot = a.state ? seq_slot(a.slots, seq, a.nslots) : -1;
-        float* st = slot >= 0 ? a.state + ((long long)slot * a.D + d) * a.N : nullptr;
-        const bool carried = st && a.carry && a.carry[seq] != 0;
-        float h[NP], A[NP];
+// B and C of one token, a block of NB states.  Their address is the same for the whole wave, so
+// the wide form reads them through the scalar cache into scalar registers, where every lane's
+// multiply takes them from: no vector register, LDS or vector-memory slot is spent on them.  It
+// needs 4-byte aligned rows and whole blocks; the other form reads element by element.
+template <typename T, int NB, bool WIDE>
+struct BcBlock {
+    static constexpr int W = WIDE ? NB * (int)sizeof(T) / 4 : NB;
+    uint32_t b[W], c[W];
+    __device__ __forceinline__ void load(const T* bp, const T* cp, int left, bool with_c) {
+        typedef const uint32_t __attribute__((address_space(4))) * scalar_ptr;
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            A[n] = n < a.N ? a.A[(long long)d * a.N + n] * kLog2e : 0.0f;
-            h[n] = carried && n < a.N ? st[n] : 0.0f;
-        }
-        const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f;
-        const float skip = a.skip ? a.skip[d] : 0.0f;
-        for (int t = start; t < end; ++t) {
-            const float xv = (float)x[t * a.ldx + d];
-            float delta = (float)dt[t * a.lddt + d] + bias;
-            if (a.softplus) delta = softplus(delta);
-            const float dx = delta * xv;
-            const T* b = Bm + t * a.ldb + (long long)g * a.N;
-            const T* c = Cm + t * a.ldc + (long long)g * a.N;
-            float out = skip * xv;
-#pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                if (n < a.N) {
-                    h[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A[n]), h[n],
-                                          dx * (float)b[n]);
-                    out = __builtin_fmaf((float)c[n], h[n], out);
-                }
+        for (int i = 0; i < W; ++i) {
+            if constexpr (WIDE) {
+                b[i] = ((scalar_ptr)(uintptr_t)bp)[i];
+                if (with_c) c[i] = ((scalar_ptr)(uintptr_t)cp)[i];
+            } else {
+                b[i] = __builtin_bit_cast(uint32_t, i < left ? (float)bp[i] : 0.0f);
+                if (with_c) c[i] = __builtin_bit_cast(uint32_t, i < left ? (float)cp[i] : 0.0f);
             }
-            if (z) out *= silu((float)z[t * a.ldz + d]);
-            y[t * a.ldy + d] = (T)out;
         }
-        if (st) {
+    }
+    // Scalar loads return in any order, so a wait for one waits for all: having this block's
+    // values here keeps the next block's loads, issued after it, out of that wait.
+    __device__ __forceinline__ void arrive(bool with_c) {
+        if constexpr (WIDE) {
+            asm volatile("" ::"s"(b[0]));
+            if (with_c) asm volatile("" ::"s"(c[0]));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    __device__ __forceinline__ static float at(const uint32_t* w, int n) {
+        if constexpr (!WIDE || sizeof(T) == 4) {
+            return __builtin_bit_cast(float, w[n]);
+        } else if constexpr (std::is_same<T, __bf16>::value) {
+            return __builtin_bit_cast(float, n & 1 ? w[n / 2] & 0xffff0000u : w[n / 2] << 16);
+        } else {
+            return (float)__builtin_bit_cast(vec_t<_Float16, 2>, w[n / 2])[n & 1];
+        }
+    }
+};
+
+// A chunk of a sequence, the work of one wave for 64 channels.
+struct Chunk {
+    int seq, first, end;  // rows [first, end)
+    int index, count;     // of the sequence's chunks
+};
+
+// Chunk c of the batch: sequence b has max(1, ceil(length / len)) chunks, numbered one sequence
+// after the other.  False behind the last.
+__device__ __forceinline__ bool find_chunk(const ScanArgs& a, int len, int c, Chunk* out) {
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int b0 = 0; b0 < a.seqs; b0 += 64) {
+        const int b = b0 + lane;
+        int n = 0;
+        if (b < a.seqs) {
+            const int rows = seq_offset(a.cu, b + 1, a.tokens) - seq_offset(a.cu, b, a.tokens);
+            n = rows > len ? (rows + len - 1) / len : 1;
+        }
+        int upto = n;  // chunks of sequences b0 .. b
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(upto, o);
+            if (lane >= o) upto += v;
+        }
+        const int k = __popcll(__ballot(base + upto <= c));
+        if (k < 64 && b0 + k < a.seqs) {
+            const int before = base + __builtin_amdgcn_readlane(upto - n, k);
+            out->seq = b0 + k;
+            out->count = __builtin_amdgcn_readlane(n, k);
+            out->index = c - before;
+            // (scalar registers: every lane has the same)
+            const int start = __builtin_amdgcn_readfirstlane(seq_offset(a.cu, out->seq, a.tokens));
+            const int end = __builtin_amdgcn_readfirstlane(seq_offset(a.cu, out->seq + 1, a.tokens));
+            out->first = start + out->index * len;
+            out->end = out->first + len < end ? out->first + len : end;
+            return true;
+        }
+        base += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+
+// Tokens of one turn of the scan's loop: the next ones are being loaded meanwhile.
+constexpr int kTurn = 4;
+
+// The scan of one chunk, in one of two passes.  A thread has one channel and its N states in
+// registers.  A sequence longer than a chunk is scanned twice, so that its chunks run at the same
+// time: LAST = false finds what a chunk adds to a state (from zero; the first chunk from the
+// sequence's own) and the sum of its steps, whose exponential is the chunk's whole decay;
+// scan_join_kernel adds up where every chunk starts; LAST = true starts there and gives outputs
+// and the sequence's final state.  Workspace: starts [chunks][N][D], then sums [chunks][D].
+template <typename T, int NP, bool WIDE, bool LAST>
+__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a, int len, int chunks, int gblocks) {
+    constexpr int NB = NP < 16 || NP % 16 != 0 || sizeof(T) == 4 ? 8 : 16;
+    const T *x = (const T*)a.x, *dt = (const T*)a.dt, *z = (const T*)a.z;
+    T* y = (T*)a.y;
+    const int per = a.D / a.groups;
+    const int cblocks = gblocks * a.groups;
+    float* starts = (float*)a.ws;
+    float* sums = starts + (long long)chunks * a.N * a.D;
+    const int c = blockIdx.x / cblocks;
+    const int cb = blockIdx.x % cblocks;
+    Chunk k;
+    if (!find_chunk(a, len, c, &k)) return;
+    if (!LAST && k.index == k.count - 1) return;
+    // channel blocks of one group: B and C are the same for the whole wave
+    const int g = cb / gblocks;
+    const int dg = (cb % gblocks) * 64 + threadIdx.x;
+    const bool live = dg < per;
+    const int d = g * per + (live ? dg : 0);
+    const int slot = a.state ? seq_slot(a.slots, k.seq, a.nslots) : -1;
+    float* st = slot >= 0 ? a.state + ((long long)slot * a.D + d) * a.N : nullptr;
+    const bool carried = st && a.carry && a.carry[k.seq] != 0;
+    float h[NP], A[NP];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        A[n] = n < a.N ? a.A[(long long)d * a.N + n] * kLog2e : 0.0f;
+        h[n] = 0.0f;
+    }
+    // (with several chunks the last one may already be writing the state)
+    if (LAST && k.count > 1) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            if (n < a.N) h[n] = starts[((long long)c * a.N + n) * a.D + d];
+    } else if (k.index == 0 && carried) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            if (n < a.N) h[n] = st[n];
+    }
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f;
+    const float skip = LAST && a.skip ? a.skip[d] : 0.0f;
+    if (!LAST && k.index == 0 && live) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            if (n < a.N) starts[((long long)c * a.N + n) * a.D + d] = h[n];
+    }
+    float sum = 0.0f;
+    const T* Bm = (const T*)a.Bm + (long long)g * a.N;
+    const T* Cm = (const T*)a.Cm + (long long)g * a.N;
+    T xs[kTurn], ds[kTurn], zs[kTurn];
+    BcBlock<T, NB, WIDE> bc;
+    auto fetch = [&](int t, T* xv, T* dv, T* zv) {
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) {
+            const long long r = t + i < k.end ? t + i : k.end - 1;
+            xv[i] = (x + r * a.ldx)[d];
+            dv[i] = (dt + r * a.lddt)[d];
+            if (LAST && z) zv[i] = (z + r * a.ldz)[d];
+        }
+    };
+    if (k.first < k.end) {
+        fetch(k.first, xs, ds, zs);
+        bc.load(Bm + k.first * a.ldb, Cm + k.first * a.ldc, a.N, LAST);
+    }
+    for (int t0 = k.first; t0 < k.end; t0 += kTurn) {
+        T xn[kTurn], dn[kTurn], zn[kTurn];
+        fetch(t0 + kTurn, xn, dn, zn);
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) {
+            // Tokens behind the end take a step of zero, which leaves the state as it is.
+            const bool here = t0 + i < k.end;
+            // (opaque here: the loop is not to be compiled once for each setting)
+            int soft = __builtin_amdgcn_readfirstlane(a.softplus);
+            int gate = __builtin_amdgcn_readfirstlane(LAST && z != nullptr);
+            asm volatile("" : "+s"(soft), "+s"(gate));
+            const float xv = (float)xs[i];
+            const float v = (float)ds[i] + bias;
+            const float sp = softplus(v);
+            float delta = soft ? sp : v;
+            delta = here ? delta : 0.0f;
+            const float dx = here ? delta * xv : 0.0f;
+            float out = skip * xv;
+            const long long next = t0 + i + 1 < k.end ? t0 + i + 1 : k.end - 1;
+#pragma unroll
+            for (int n0 = 0; n0 < NP; n0 += NB) {
+                BcBlock<T, NB, WIDE> nb;
+                bc.arrive(LAST);
+                if (n0 + NB < NP) {
+                    const long long r = here ? t0 + i : k.end - 1;
+                    nb.load(Bm + r * a.ldb + n0 + NB, Cm + r * a.ldc + n0 + NB, a.N - n0 - NB,
+                            LAST);
+                } else {
+                    nb.load(Bm + next * a.ldb, Cm + next * a.ldc, a.N, LAST);
+                }
+                if constexpr (WIDE) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const float e = __builtin_amdgcn_exp2f(delta * A[n0 + n]);
+                    h[n0 + n] = __builtin_fmaf(e, h[n0 + n], dx * bc.at(bc.b, n));
+                    if (LAST) out = __builtin_fmaf(bc.at(bc.c, n), h[n0 + n], out);
+                }
+                bc = nb;
+            }
+            if (LAST) {
+                if (gate) out *= silu((float)zs[i]);
+                if (here && live) (y + (t0 + i) * a.ldy)[d] = (T)out;
+            } else {
+                sum += delta;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) xs[i] = xn[i], ds[i] = dn[i], zs[i] = zn[i];
+    }
+    if (!live) return;
+    if (LAST) {
+        if (st && k.index == k.count - 1) {
 #pragma unroll
             for (int n = 0; n < NP; ++n)
                 if (n < a.N) st[n] = h[n];
+        }
+    } else if (c + 1 < chunks) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            if (n < a.N) starts[((long long)(c + 1) * a.N + n) * a.D + d] = h[n];
+        sums[(long long)c * a.D + d] = sum;
+    }
+}
+
+// Where a sequence's chunks start: start[j] = (what chunk j-1 added) + decay(j-1) * start[j-1].
+// The first pass left the starts of chunks 0 and 1 whole.  One thread per (sequence, state,
+// channel) goes along the chunks, kJoin of them loaded at a time.
+constexpr int kJoin = 8;
+__global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a, int len, int chunks,
+                                                        int blocks, long long units) {
+    float* starts = (float*)a.ws;
+    const float* sums = starts + (long long)chunks * a.N * a.D;
+    const long long plane = (long long)a.N * a.D;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int seq = (int)(u / blocks);
+        const int i = (int)(u % blocks) * 256 + threadIdx.x;
+        const int lane = threadIdx.x & 63;
+        int before = 0, count = 0;  // chunks of the sequences before it, and its own
+        for (int b0 = 0; b0 <= seq; b0 += 64) {
+            const int b = b0 + lane;
+            int n = 0;
+            if (b <= seq) {
+                const int rows = seq_offset(a.cu, b + 1, a.tokens) - seq_offset(a.cu, b, a.tokens);
+                n = rows > len ? (rows + len - 1) / len : 1;
+            }
+            if (b == seq) count = n;
+            int all = b < seq ? n : 0;
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o);
+            before += all;
+        }
+        count = __shfl(count, seq & 63);
+        if (before + count > chunks) count = chunks - before;
+        if (count <= 2 || i >= plane) continue;
+        const int d = i % a.D;
+        const float A = a.A[(long long)d * a.N + i / a.D] * kLog2e;
+        float* s = starts + (long long)before * plane + i;
+        const float* w = sums + (long long)before * a.D + d;
+        float h = s[plane];
+        for (int j = 2; j < count; j += kJoin) {
+            float add[kJoin], sum[kJoin];
+#pragma unroll
+            for (int q = 0; q < kJoin; ++q) {
+                const int c = j + q < count ? j + q : count - 1;
+                add[q] = s[c * plane];
+                sum[q] = w[(long long)(c - 1) * a.D];
+            }
+#pragma unroll
+            for (int q = 0; q < kJoin; ++q) {
+                if (j + q < count) {
+                    h = __builtin_fmaf(__builtin_amdgcn_exp2f(sum[q] * A), h, add[q]);
+                    s[(j + q) * plane] = h;
+                }
+            }
         }
     }
 }
@@ -98,40 +320,86 @@ __global__ __launch_bounds__(64) void scan_step_kernel(ScanArgs a, int cblocks, 
     }
 }
 
-template <typename T>
-int pick_states(const ScanArgs& a, bool step, void* stream) {
-    const int cblocks = (a.D + 63) / 64;
-    const long long units = (long long)a.seqs * cblocks;
-    const int grid = (int)(units < (1 << 22) ? units : (1 << 22));
-    hipStream_t s = (hipStream_t)stream;
-    auto go = [&](auto np) {
-        constexpr int NP = decltype(np)::value;
-        if (step)
-            scan_step_kernel<T, NP><<<grid, 64, 0, s>>>(a, cblocks, units);
-        else
-            scan_fwd_kernel<T, NP><<<grid, 64, 0, s>>>(a, cblocks, units);
-        return (int)hipGetLastError();
-    };
-    if (a.N <= 8) return go(std::integral_constant<int, 8>());
-    if (a.N <= 16) return go(std::integral_constant<int, 16>());
-    if (a.N <= 32) return go(std::integral_constant<int, 32>());
-    return go(std::integral_constant<int, 64>());
+// Tokens of a chunk.  One wave scans 64 channels of a chunk, and the card's 1024 SIMDs want about
+// four of them each to hide memory and instruction latency; a shorter chunk than that only costs
+// more starts to hand on, and one that holds the longest sequence possible spares the first pass.
+int chunk_len(int tokens, int D, int groups) {
+    const long long cblocks = (long long)((D / groups + 63) / 64) * groups;
+    const long long want = tokens * cblocks / 4096;
+    int len = 32;
+    while ((len < want && len < 256) || tokens / len * cblocks > (1 << 25)) len *= 2;
+    return len;
 }
 
-int pick(const ScanArgs& a, int dtype, bool step, void* stream) {
-    if (dtype == FCM_F32) return pick_states<float>(a, step, stream);
-    if (dtype == FCM_F16) return pick_states<_Float16>(a, step, stream);
-    return pick_states<__bf16>(a, step, stream);
+int grid_of(long long units) { return (int)(units < (1 << 22) ? units : (1 << 22)); }
+
+template <typename T, int NP, bool WIDE>
+int run_fwd(const ScanArgs& a, hipStream_t s) {
+    const int len = chunk_len(a.tokens, a.D, a.groups);
+    const int chunks = a.tokens / len + a.seqs;
+    const int gblocks = (a.D / a.groups + 63) / 64;
+    const int grid = chunks * gblocks * a.groups;
+    if (a.tokens > len) {
+        scan_fwd_kernel<T, NP, WIDE, false><<<grid, 64, 0, s>>>(a, len, chunks, gblocks);
+        if (a.tokens > 2 * len) {
+            const int blocks = (int)(((long long)a.N * a.D + 255) / 256);
+            const long long joins = (long long)a.seqs * blocks;
+            scan_join_kernel<<<grid_of(joins), 256, 0, s>>>(a, len, chunks, blocks, joins);
+        }
+    }
+    scan_fwd_kernel<T, NP, WIDE, true><<<grid, 64, 0, s>>>(a, len, chunks, gblocks);
+    return (int)hipGetLastError();
+}
+
+template <typename T>
+int fwd_states(const ScanArgs& a, hipStream_t s) {
+    const bool rows4 = ((uintptr_t)a.Bm & 3) == 0 && ((uintptr_t)a.Cm & 3) == 0 &&
+                       (a.ldb * sizeof(T)) % 4 == 0 && (a.ldc * sizeof(T)) % 4 == 0;
+    if (rows4) {
+        if (a.N == 8) return run_fwd<T, 8, true>(a, s);
+        if (a.N == 16) return run_fwd<T, 16, true>(a, s);
+        if (a.N == 24) return run_fwd<T, 24, true>(a, s);
+        if (a.N == 32) return run_fwd<T, 32, true>(a, s);
+        if (a.N == 48) return run_fwd<T, 48, true>(a, s);
+        if (a.N == 64) return run_fwd<T, 64, true>(a, s);
+    }
+    if (a.N <= 8) return run_fwd<T, 8, false>(a, s);
+    if (a.N <= 16) return run_fwd<T, 16, false>(a, s);
+    if (a.N <= 32) return run_fwd<T, 32, false>(a, s);
+    return run_fwd<T, 64, false>(a, s);
+}
+
+template <typename T>
+int step_states(const ScanArgs& a, hipStream_t s) {
+    const int cblocks = (a.D + 63) / 64;
+    const long long units = (long long)a.seqs * cblocks;
+    const int grid = grid_of(units);
+    if (a.N <= 8) scan_step_kernel<T, 8><<<grid, 64, 0, s>>>(a, cblocks, units);
+    else if (a.N <= 16) scan_step_kernel<T, 16><<<grid, 64, 0, s>>>(a, cblocks, units);
+    else if (a.N <= 32) scan_step_kernel<T, 32><<<grid, 64, 0, s>>>(a, cblocks, units);
+    else scan_step_kernel<T, 64><<<grid, 64, 0, s>>>(a, cblocks, units);
+    return (int)hipGetLastError();
 }
 
 }  // namespace
 
 int launch_scan_fwd(const ScanArgs& a, int dtype, void* stream) {
-    return pick(a, dtype, false, stream);
+    hipStream_t s = (hipStream_t)stream;
+    if (dtype == FCM_F32) return fwd_states<float>(a, s);
+    if (dtype == FCM_F16) return fwd_states<_Float16>(a, s);
+    return fwd_states<__bf16>(a, s);
 }
 int launch_scan_step(const ScanArgs& a, int dtype, void* stream) {
-    return pick(a, dtype, true, stream);
+    hipStream_t s = (hipStream_t)stream;
+    if (dtype == FCM_F32) return step_states<float>(a, s);
+    if (dtype == FCM_F16) return step_states<_Float16>(a, s);
+    return step_states<__bf16>(a, s);
 }
-long long scan_workspace_bytes(const fcm_scan_problem&) { return 0; }
+long long scan_workspace_bytes(const fcm_scan_problem& p) {
+    const int groups = p.groups > 0 ? p.groups : 1;
+    const int len = chunk_len(p.tokens, p.D, groups);
+    if (p.tokens <= len) return 0;
+    return (long long)(p.tokens / len + p.seqs) * p.D * (p.N + 1) * 4;
+}
 
 }  // namespace fcm
