@@ -9,46 +9,34 @@ namespace {
 
 constexpr float kLog2e = 1.44269504f;
 
-// B and C of one token, a block of NB states.  Their address is the same for the whole wave, so
-// the wide form reads them through the scalar cache into scalar registers, where every lane's
-// multiply takes them from: no vector register, LDS or vector-memory slot is spent on them.  It
-// needs 4-byte aligned rows and whole blocks; the other form reads element by element.
-template <typename T, int NB, bool WIDE>
-struct BcBlock {
-    static constexpr int W = WIDE ? NB * (int)sizeof(T) / 4 : NB;
-    uint32_t b[W], c[W];
-    __device__ __forceinline__ void load(const T* bp, const T* cp, int left, bool with_c) {
-        typedef const uint32_t __attribute__((address_space(4))) * scalar_ptr;
+// A channel's N <= NP values: in 16-byte pieces (`wide`: N is a multiple of 4 and the array 16-byte
+// aligned), or one by one.
+template <int NP>
+__device__ __forceinline__ void load_states(const float* p, int N, bool wide, float* v) {
+    if (wide) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if constexpr (WIDE) {
-                b[i] = ((scalar_ptr)(uintptr_t)bp)[i];
-                if (with_c) c[i] = ((scalar_ptr)(uintptr_t)cp)[i];
-            } else {
-                b[i] = __builtin_bit_cast(uint32_t, i < left ? (float)bp[i] : 0.0f);
-                if (with_c) c[i] = __builtin_bit_cast(uint32_t, i < left ? (float)cp[i] : 0.0f);
-            }
+        for (int q = 0; q < NP / 4; ++q) {
+            const f32x4 w = 4 * q < N ? *(const f32x4*)(p + 4 * q) : f32x4{};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * q + j] = w[j];
         }
+    } else {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) v[n] = n < N ? p[n] : 0.0f;
     }
-    // Scalar loads return in any order, so a wait for one waits for all: having this block's
-    // values here keeps the next block's loads, issued after it, out of that wait.
-    __device__ __forceinline__ void arrive(bool with_c) {
-        if constexpr (WIDE) {
-            asm volatile("" ::"s"(b[0]));
-            if (with_c) asm volatile("" ::"s"(c[0]));
-            __builtin_amdgcn_sched_barrier(0);
-        }
+}
+template <int NP>
+__device__ __forceinline__ void store_states(float* p, int N, bool wide, const float* v) {
+    if (wide) {
+#pragma unroll
+        for (int q = 0; q < NP / 4; ++q)
+            if (4 * q < N) *(f32x4*)(p + 4 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    } else {
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+            if (n < N) p[n] = v[n];
     }
-    __device__ __forceinline__ static float at(const uint32_t* w, int n) {
-        if constexpr (!WIDE || sizeof(T) == 4) {
-            return __builtin_bit_cast(float, w[n]);
-        } else if constexpr (std::is_same<T, __bf16>::value) {
-            return __builtin_bit_cast(float, n & 1 ? w[n / 2] & 0xffff0000u : w[n / 2] << 16);
-        } else {
-            return (float)__builtin_bit_cast(vec_t<_Float16, 2>, w[n / 2])[n & 1];
-        }
-    }
-};
+}
 
 // A chunk of a sequence, the work of one wave for 64 channels.
 struct Chunk {
@@ -94,6 +82,13 @@ __device__ __forceinline__ bool find_chunk(const ScanArgs& a, int len, int c, Ch
 
 // Tokens of one turn of the scan's loop: the next ones are being loaded meanwhile.
 constexpr int kTurn = 4;
+constexpr int kScanWaves = 4;  // waves of a workgroup, 64 channels each
+
+// Tokens whose B and C a workgroup holds in LDS at a time: 16 KB of fp32.
+template <int NP>
+constexpr int scan_tile() {
+    return 16384 / (2 * NP * 4) / kTurn * kTurn;
+}
 
 // The scan of one chunk, in one of two passes.  A thread has one channel and its N states in
 // registers.  A sequence longer than a chunk is scanned twice, so that its chunks run at the same
@@ -101,11 +96,15 @@ constexpr int kTurn = 4;
 // sequence's own) and the sum of its steps, whose exponential is the chunk's whole decay;
 // scan_join_kernel adds up where every chunk starts; LAST = true starts there and gives outputs
 // and the sequence's final state.  Workspace: starts [chunks][N][D], then sums [chunks][D].
-template <typename T, int NP, bool WIDE, bool LAST>
-__global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a, int len, int chunks, int gblocks) {
-    constexpr int NB = NP < 16 || NP % 16 != 0 || sizeof(T) == 4 ? 8 : 16;
-    const T *x = (const T*)a.x, *dt = (const T*)a.dt, *z = (const T*)a.z;
-    T* y = (T*)a.y;
+//
+// B and C are the same for all channels of a group: the workgroup converts them to fp32 in LDS
+// once a tile, and its lanes read them by broadcast, four states an instruction.
+template <typename T, int NP, bool LAST>
+__global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a, int len, int chunks,
+                                                                   int gblocks, bool wide) {
+    constexpr int TILE = scan_tile<NP>();
+    __shared__ f32x4 bc[TILE][(LAST ? 2 : 1) * NP / 4];
+    const bool gate = LAST && a.z != nullptr;
     const int per = a.D / a.groups;
     const int cblocks = gblocks * a.groups;
     float* starts = (float*)a.ws;
@@ -115,18 +114,38 @@ __global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a, int len, int c
     Chunk k;
     if (!find_chunk(a, len, c, &k)) return;
     if (!LAST && k.index == k.count - 1) return;
-    // channel blocks of one group: B and C are the same for the whole wave
+    // channel blocks of one group: B and C are the same for the whole workgroup
     const int g = cb / gblocks;
-    const int dg = (cb % gblocks) * 64 + threadIdx.x;
+    const int dg = (cb % gblocks) * blockDim.x + threadIdx.x;
     const bool live = dg < per;
     const int d = g * per + (live ? dg : 0);
+    // Row pointers, the same for the whole wave; they stay on the last row once they are there.
+    const T* px = (const T*)a.x + k.first * a.ldx;
+    const T* pd = (const T*)a.dt + k.first * a.lddt;
+    const T* pz = gate ? (const T*)a.z + k.first * a.ldz : nullptr;
+    T* py = (T*)a.y + k.first * a.ldy;
+    T xs[kTurn], ds[kTurn], zs[kTurn];
+    auto fetch = [&](int t, T* xv, T* dv, T* zv) {
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) {
+            xv[i] = px[d];
+            dv[i] = pd[d];
+            if (gate) zv[i] = pz[d];
+            const bool more = t + i + 1 < k.end;
+            px += more ? a.ldx : 0;
+            pd += more ? a.lddt : 0;
+            if (gate) pz += more ? a.ldz : 0;
+        }
+    };
+    if (k.first < k.end) fetch(k.first, xs, ds, zs);
     const int slot = a.state ? seq_slot(a.slots, k.seq, a.nslots) : -1;
     float* st = slot >= 0 ? a.state + ((long long)slot * a.D + d) * a.N : nullptr;
     const bool carried = st && a.carry && a.carry[k.seq] != 0;
     float h[NP], A[NP];
+    load_states<NP>(a.A + (long long)d * a.N, a.N, wide, A);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-        A[n] = n < a.N ? a.A[(long long)d * a.N + n] * kLog2e : 0.0f;
+        A[n] *= kLog2e;
         h[n] = 0.0f;
     }
     // (with several chunks the last one may already be writing the state)
@@ -135,9 +154,7 @@ __global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a, int len, int c
         for (int n = 0; n < NP; ++n)
             if (n < a.N) h[n] = starts[((long long)c * a.N + n) * a.D + d];
     } else if (k.index == 0 && carried) {
-#pragma unroll
-        for (int n = 0; n < NP; ++n)
-            if (n < a.N) h[n] = st[n];
+        load_states<NP>(st, a.N, wide, h);
     }
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f;
     const float skip = LAST && a.skip ? a.skip[d] : 0.0f;
@@ -147,79 +164,64 @@ __global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a, int len, int c
             if (n < a.N) starts[((long long)c * a.N + n) * a.D + d] = h[n];
     }
     float sum = 0.0f;
-    const T* Bm = (const T*)a.Bm + (long long)g * a.N;
-    const T* Cm = (const T*)a.Cm + (long long)g * a.N;
-    T xs[kTurn], ds[kTurn], zs[kTurn];
-    BcBlock<T, NB, WIDE> bc;
-    auto fetch = [&](int t, T* xv, T* dv, T* zv) {
-#pragma unroll
-        for (int i = 0; i < kTurn; ++i) {
-            const long long r = t + i < k.end ? t + i : k.end - 1;
-            xv[i] = (x + r * a.ldx)[d];
-            dv[i] = (dt + r * a.lddt)[d];
-            if (LAST && z) zv[i] = (z + r * a.ldz)[d];
+    for (int tile = k.first; tile < k.end; tile += TILE) {
+        const int rows = tile + TILE < k.end ? TILE : k.end - tile;
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * NP; i += blockDim.x) {
+            const int t = i / NP, n = i % NP;
+            const long long r = tile + t;
+            const bool in = n < a.N;
+            const T* b = (const T*)a.Bm + r * a.ldb + (long long)g * a.N + n;
+            const T* cc = (const T*)a.Cm + r * a.ldc + (long long)g * a.N + n;
+            float* to = (float*)bc[t];
+            to[n] = in ? (float)*b : 0.0f;
+            if (LAST) to[NP + n] = in ? (float)*cc : 0.0f;
         }
-    };
-    if (k.first < k.end) {
-        fetch(k.first, xs, ds, zs);
-        bc.load(Bm + k.first * a.ldb, Cm + k.first * a.ldc, a.N, LAST);
-    }
-    for (int t0 = k.first; t0 < k.end; t0 += kTurn) {
-        T xn[kTurn], dn[kTurn], zn[kTurn];
-        fetch(t0 + kTurn, xn, dn, zn);
+        __syncthreads();
+        for (int t0 = 0; t0 < rows; t0 += kTurn) {
+            T xn[kTurn], dn[kTurn], zn[kTurn];
+            fetch(tile + t0 + kTurn, xn, dn, zn);
 #pragma unroll
-        for (int i = 0; i < kTurn; ++i) {
-            // Tokens behind the end take a step of zero, which leaves the state as it is.
-            const bool here = t0 + i < k.end;
-            // (opaque here: the loop is not to be compiled once for each setting)
-            int soft = __builtin_amdgcn_readfirstlane(a.softplus);
-            int gate = __builtin_amdgcn_readfirstlane(LAST && z != nullptr);
-            asm volatile("" : "+s"(soft), "+s"(gate));
-            const float xv = (float)xs[i];
-            const float v = (float)ds[i] + bias;
-            const float sp = softplus(v);
-            float delta = soft ? sp : v;
-            delta = here ? delta : 0.0f;
-            const float dx = here ? delta * xv : 0.0f;
-            float out = skip * xv;
-            const long long next = t0 + i + 1 < k.end ? t0 + i + 1 : k.end - 1;
+            for (int i = 0; i < kTurn; ++i) {
+                // Tokens behind the end take a step of zero, which leaves the state as it is
+                // (their row of the tile is an old one, or the last).
+                const bool here = t0 + i < rows;
+                const f32x4* row = bc[here ? t0 + i : rows - 1];
+                const float xv = (float)xs[i];
+                const float v = (float)ds[i] + bias;
+                const float sp = softplus(v);
+                float delta = a.softplus ? sp : v;
+                delta = here ? delta : 0.0f;
+                const float dx = here ? delta * xv : 0.0f;
+                float out = skip * xv;
 #pragma unroll
-            for (int n0 = 0; n0 < NP; n0 += NB) {
-                BcBlock<T, NB, WIDE> nb;
-                bc.arrive(LAST);
-                if (n0 + NB < NP) {
-                    const long long r = here ? t0 + i : k.end - 1;
-                    nb.load(Bm + r * a.ldb + n0 + NB, Cm + r * a.ldc + n0 + NB, a.N - n0 - NB,
-                            LAST);
+                for (int q = 0; q < NP / 4; ++q) {
+                    const f32x4 B = row[q];
+                    f32x4 C;
+                    if (LAST) C = row[NP / 4 + q];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int n = 4 * q + j;
+                        const float e = __builtin_amdgcn_exp2f(delta * A[n]);
+                        h[n] = __builtin_fmaf(e, h[n], dx * B[j]);
+                        if (LAST) out = __builtin_fmaf(C[j], h[n], out);
+                    }
+                }
+                if (LAST) {
+                    if (gate) out *= silu((float)zs[i]);
+                    if (here && live) py[d] = (T)out;
+                    py += a.ldy;
                 } else {
-                    nb.load(Bm + next * a.ldb, Cm + next * a.ldc, a.N, LAST);
+                    sum += delta;
                 }
-                if constexpr (WIDE) __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
-                    const float e = __builtin_amdgcn_exp2f(delta * A[n0 + n]);
-                    h[n0 + n] = __builtin_fmaf(e, h[n0 + n], dx * bc.at(bc.b, n));
-                    if (LAST) out = __builtin_fmaf(bc.at(bc.c, n), h[n0 + n], out);
-                }
-                bc = nb;
-            }
-            if (LAST) {
-                if (gate) out *= silu((float)zs[i]);
-                if (here && live) (y + (t0 + i) * a.ldy)[d] = (T)out;
-            } else {
-                sum += delta;
-            }
+            for (int i = 0; i < kTurn; ++i) xs[i] = xn[i], ds[i] = dn[i], zs[i] = zn[i];
         }
-#pragma unroll
-        for (int i = 0; i < kTurn; ++i) xs[i] = xn[i], ds[i] = dn[i], zs[i] = zn[i];
     }
     if (!live) return;
     if (LAST) {
-        if (st && k.index == k.count - 1) {
-#pragma unroll
-            for (int n = 0; n < NP; ++n)
-                if (n < a.N) st[n] = h[n];
-        }
+        if (st && k.index == k.count - 1) store_states<NP>(st, a.N, wide, h);
     } else if (c + 1 < chunks) {
 #pragma unroll
         for (int n = 0; n < NP; ++n)
@@ -230,17 +232,16 @@ __global__ __launch_bounds__(64) void scan_fwd_kernel(ScanArgs a, int len, int c
 
 // Where a sequence's chunks start: start[j] = (what chunk j-1 added) + decay(j-1) * start[j-1].
 // The first pass left the starts of chunks 0 and 1 whole.  One thread per (sequence, state,
-// channel) goes along the chunks, kJoin of them loaded at a time.
-constexpr int kJoin = 8;
+// channel) goes along the chunks, kJoin of them at a time while the next are being loaded.
+constexpr int kJoin = 16;
 __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a, int len, int chunks,
                                                         int blocks, long long units) {
     float* starts = (float*)a.ws;
     const float* sums = starts + (long long)chunks * a.N * a.D;
     const long long plane = (long long)a.N * a.D;
+    const int lane = threadIdx.x & 63;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const int seq = (int)(u / blocks);
-        const int i = (int)(u % blocks) * 256 + threadIdx.x;
-        const int lane = threadIdx.x & 63;
         int before = 0, count = 0;  // chunks of the sequences before it, and its own
         for (int b0 = 0; b0 <= seq; b0 += 64) {
             const int b = b0 + lane;
@@ -257,27 +258,34 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a, int len, int
         }
         count = __shfl(count, seq & 63);
         if (before + count > chunks) count = chunks - before;
+        const long long i = (u % blocks) * 256 + threadIdx.x;
         if (count <= 2 || i >= plane) continue;
-        const int d = i % a.D;
+        const int d = (int)(i % a.D);
         const float A = a.A[(long long)d * a.N + i / a.D] * kLog2e;
         float* s = starts + (long long)before * plane + i;
         const float* w = sums + (long long)before * a.D + d;
-        float h = s[plane];
-        for (int j = 2; j < count; j += kJoin) {
-            float add[kJoin], sum[kJoin];
+        float add[kJoin], sum[kJoin];
+        auto fetch = [&](int j) {
 #pragma unroll
             for (int q = 0; q < kJoin; ++q) {
                 const int c = j + q < count ? j + q : count - 1;
                 add[q] = s[c * plane];
                 sum[q] = w[(long long)(c - 1) * a.D];
             }
+        };
+        float h = s[plane];
+        fetch(2);
+        for (int j = 2; j < count; j += kJoin) {
+            float start[kJoin];
 #pragma unroll
             for (int q = 0; q < kJoin; ++q) {
-                if (j + q < count) {
-                    h = __builtin_fmaf(__builtin_amdgcn_exp2f(sum[q] * A), h, add[q]);
-                    s[(j + q) * plane] = h;
-                }
+                h = __builtin_fmaf(__builtin_amdgcn_exp2f(sum[q] * A), h, add[q]);
+                start[q] = h;
             }
+            if (j + kJoin < count) fetch(j + kJoin);
+#pragma unroll
+            for (int q = 0; q < kJoin; ++q)
+                if (j + q < count) s[(j + q) * plane] = start[q];
         }
     }
 }
@@ -325,7 +333,7 @@ __global__ __launch_bounds__(64) void scan_step_kernel(ScanArgs a, int cblocks, 
 // more starts to hand on, and one that holds the longest sequence possible spares the first pass.
 int chunk_len(int tokens, int D, int groups) {
     const long long cblocks = (long long)((D / groups + 63) / 64) * groups;
-    const long long want = tokens * cblocks / 4096;
+    const long long want = tokens * cblocks / 8192;
     int len = 32;
     while ((len < want && len < 256) || tokens / len * cblocks > (1 << 25)) len *= 2;
     return len;
@@ -333,40 +341,35 @@ int chunk_len(int tokens, int D, int groups) {
 
 int grid_of(long long units) { return (int)(units < (1 << 22) ? units : (1 << 22)); }
 
-template <typename T, int NP, bool WIDE>
+template <typename T, int NP>
 int run_fwd(const ScanArgs& a, hipStream_t s) {
     const int len = chunk_len(a.tokens, a.D, a.groups);
     const int chunks = a.tokens / len + a.seqs;
-    const int gblocks = (a.D / a.groups + 63) / 64;
+    const int waves = (a.D / a.groups + 63) / 64;
+    const int block = 64 * (waves < kScanWaves ? waves : kScanWaves);
+    const int gblocks = (a.D / a.groups + block - 1) / block;
     const int grid = chunks * gblocks * a.groups;
+    const bool wide = a.N % 4 == 0 && (((uintptr_t)a.A | (uintptr_t)a.state) & 15) == 0;
     if (a.tokens > len) {
-        scan_fwd_kernel<T, NP, WIDE, false><<<grid, 64, 0, s>>>(a, len, chunks, gblocks);
+        scan_fwd_kernel<T, NP, false><<<grid, block, 0, s>>>(a, len, chunks, gblocks, wide);
         if (a.tokens > 2 * len) {
             const int blocks = (int)(((long long)a.N * a.D + 255) / 256);
             const long long joins = (long long)a.seqs * blocks;
             scan_join_kernel<<<grid_of(joins), 256, 0, s>>>(a, len, chunks, blocks, joins);
         }
     }
-    scan_fwd_kernel<T, NP, WIDE, true><<<grid, 64, 0, s>>>(a, len, chunks, gblocks);
+    scan_fwd_kernel<T, NP, true><<<grid, block, 0, s>>>(a, len, chunks, gblocks, wide);
     return (int)hipGetLastError();
 }
 
 template <typename T>
 int fwd_states(const ScanArgs& a, hipStream_t s) {
-    const bool rows4 = ((uintptr_t)a.Bm & 3) == 0 && ((uintptr_t)a.Cm & 3) == 0 &&
-                       (a.ldb * sizeof(T)) % 4 == 0 && (a.ldc * sizeof(T)) % 4 == 0;
-    if (rows4) {
-        if (a.N == 8) return run_fwd<T, 8, true>(a, s);
-        if (a.N == 16) return run_fwd<T, 16, true>(a, s);
-        if (a.N == 24) return run_fwd<T, 24, true>(a, s);
-        if (a.N == 32) return run_fwd<T, 32, true>(a, s);
-        if (a.N == 48) return run_fwd<T, 48, true>(a, s);
-        if (a.N == 64) return run_fwd<T, 64, true>(a, s);
-    }
-    if (a.N <= 8) return run_fwd<T, 8, false>(a, s);
-    if (a.N <= 16) return run_fwd<T, 16, false>(a, s);
-    if (a.N <= 32) return run_fwd<T, 32, false>(a, s);
-    return run_fwd<T, 64, false>(a, s);
+    if (a.N <= 8) return run_fwd<T, 8>(a, s);
+    if (a.N <= 16) return run_fwd<T, 16>(a, s);
+    if (a.N <= 24) return run_fwd<T, 24>(a, s);
+    if (a.N <= 32) return run_fwd<T, 32>(a, s);
+    if (a.N <= 48) return run_fwd<T, 48>(a, s);
+    return run_fwd<T, 64>(a, s);
 }
 
 template <typename T>
