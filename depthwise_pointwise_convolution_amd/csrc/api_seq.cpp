@@ -267,8 +267,8 @@ fcm_status fcm_q4_fwd(const fcm_q4_problem* prob, const void* x, const void* q,
     if (p.group != 32 && p.group != 64 && p.group != 128)
         return unsupported("groups have 32, 64 or 128 channels");
     if (p.act < FCM_ACT_NONE || p.act > FCM_ACT_RELU6) return invalid("act is not an fcm_act");
-    if (p.C > (1 << 20) || p.K > (1 << 24) || p.M > (1 << 24))
-        return unsupported("C above 2^20, K or M above 2^24");
+    if (p.C > (1 << 20) || p.M > (1 << 20) || p.K > (1 << 24))
+        return unsupported("C or M above 2^20, K above 2^24");
     Q4Args a;
     memset(&a, 0, sizeof(a));
     a.ldx = p.ldx;
@@ -276,6 +276,7 @@ fcm_status fcm_q4_fwd(const fcm_q4_problem* prob, const void* x, const void* q,
     SEQ_TRY(stride(&a.ldx, p.C));
     SEQ_TRY(stride(&a.ldy, p.K));
     if (a.ldx % 8 != 0) return invalid("ldx must be a multiple of 8");
+    if (a.ldx >= (1ll << 26)) return unsupported("ldx of 2^26 or more");
     NEED(q, 4);
     NEED(scales, 2);
     MAYBE(bias, 4);
