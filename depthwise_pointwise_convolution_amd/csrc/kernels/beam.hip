@@ -9,100 +9,244 @@
 namespace fcm {
 namespace {
 
-// What selection keeps of a logits row: its log-sum-exp, and its best tokens, best first.
-struct RowHead {
-    double lse;
-    double pad;
-};
-struct Cand {
-    float logit;
-    int token;  // -1: the vocabulary has no more
-};
-
-__host__ __device__ inline long long row_bytes(int beams) {
-    return (long long)sizeof(RowHead) + ((long long)beams * sizeof(Cand) + 15) / 16 * 16;
+// Selection works on keys that order as integers: a float's bits turned so that they ascend, and
+// below them the complement of the token, so that among equal logits the lowest token is largest.
+// 0 is below every key.
+typedef uint64_t Key;
+__device__ __forceinline__ uint32_t ascending(float f) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);  // (-0 is 0)
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-
-__device__ __forceinline__ bool before(float v, int i, float w, int j) {
-    return v > w || (v == w && i < j);
+__device__ __forceinline__ float from_ascending(uint32_t u) {
+    return __builtin_bit_cast(float, u ^ (u >> 31 ? 0x80000000u : 0xffffffffu));
 }
-
-template <typename T>
-__device__ __forceinline__ float clean(T v) {
-    const float f = (float)v;
-    return f != f ? -__builtin_inff() : __builtin_fminf(f, FLT_MAX);
+__device__ __forceinline__ Key make_key(float f, int token) {
+    return (Key)ascending(f) << 32 | (uint32_t)~token;
 }
+__device__ __forceinline__ int key_token(Key k) { return (int)~(uint32_t)k; }
+__device__ __forceinline__ float key_logit(Key k) { return from_ascending((uint32_t)(k >> 32)); }
 
-// One workgroup per row: a pass for the log-sum-exp, then one pass for each kept token.
-template <typename T>
-__global__ __launch_bounds__(256) void beam_rows_kernel(BeamArgs a) {
-    __shared__ float sv[4];
-    __shared__ int si[4];
-    __shared__ double sd[4];
-    const int row = blockIdx.x, tid = threadIdx.x, wave = tid >> 6;
-    const T* l = (const T*)a.logits + row * a.ldl;
-    char* out = (char*)a.ws + row * row_bytes(a.beams);
-    Cand* cand = (Cand*)(out + sizeof(RowHead));
-    float top = 0.0f;
-    float pv = __builtin_inff();
-    int pi = -1;
-    for (int k = 0; k < a.beams; ++k) {
-        // the best candidate behind (pv, pi)
-        float bv = -__builtin_inff();
-        int bi = INT_MAX;
-        for (int v = tid; v < a.vocab; v += 256) {
-            const float f = clean(l[v]);
-            if (before(pv, pi, f, v) && before(f, v, bv, bi)) bv = f, bi = v;
-        }
+// Largest of the wave's 64 values: shifts within rows of 16 lanes, then from row to row.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define FCM_DPP_MAX(ctrl, rows)                                                            \
+    {                                                                                      \
+        const uint32_t o = __builtin_amdgcn_update_dpp(0u, v, ctrl, rows, 0xf, false);     \
+        v = v > o ? v : o;                                                                 \
+    }
+    FCM_DPP_MAX(0x111, 0xf)  // row_shr 1, 2, 4, 8
+    FCM_DPP_MAX(0x112, 0xf)
+    FCM_DPP_MAX(0x114, 0xf)
+    FCM_DPP_MAX(0x118, 0xf)
+    FCM_DPP_MAX(0x142, 0xa)  // last lane of a row to the next row
+    FCM_DPP_MAX(0x143, 0xc)  // last lane of the lower half to the upper
+#undef FCM_DPP_MAX
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ Key wave_max(Key k) {
+    const uint32_t hi = wave_max((uint32_t)(k >> 32));
+    const uint32_t lo = wave_max((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return (Key)hi << 32 | lo;
+}
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) {
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const float v = __shfl_xor(bv, o);
-            const int i = __shfl_xor(bi, o);
-            if (before(v, i, bv, bi)) bv = v, bi = i;
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+// A wave looks at kBlock tokens of a row at a time, kLane of them in a lane's registers; one
+// wave's tokens are a split, of which a row has at most 64.
+constexpr int kLane = 32;
+constexpr int kBlock = 64 * kLane;
+// What selection keeps of a split: its largest logit, the sum of exp(logit - largest), and its
+// best tokens as keys, best first.
+struct SplitHead {
+    float top, sum;
+};
+__host__ __device__ inline long long split_bytes(int beams) {
+    return (long long)sizeof(SplitHead) + (long long)beams * sizeof(Key);
+}
+__host__ __device__ inline int split_blocks(int vocab) {
+    const int blocks = (vocab + kBlock - 1) / kBlock;
+    return (blocks + 63) / 64;
+}
+__host__ __device__ inline int row_splits(int vocab) {
+    const int per = split_blocks(vocab) * kBlock;
+    return (vocab + per - 1) / per;
+}
+
+// One wave per (row, split): one reading of the logits.  The W-th largest of the 64 lanes' own
+// maxima is a bound that W tokens reach, so only tokens that reach it can be among the best W: a
+// dozen or so, gathered through LDS and ranked against each other.  Where many tokens are equal
+// (a masked row, coarse logits) more than 64 may reach it; then the best are taken one by one.
+template <typename T>
+__global__ __launch_bounds__(256) void beam_rows_kernel(BeamArgs a, int splits, int blocks) {
+    __shared__ Key pool[4][64], best[4][32];
+    constexpr int VE = Vec<T>::N;
+    const float inf = __builtin_inff();
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int id = blockIdx.x * 4 + wave;
+    const int row = id / splits, split = id % splits, W = a.beams;
+    if (row >= a.requests * W) return;
+    const T* l = (const T*)a.logits + row * a.ldl;
+    Key mine = 0;  // lane r: the r-th best so far
+    int have = 0;
+    float top = -inf, sum = 0.0f;
+    for (int b = 0; b < blocks; ++b) {
+        const int base = (split * blocks + b) * kBlock;
+        if (base >= a.vocab) break;
+        float v[kLane];
+#pragma unroll
+        for (int j = 0; j < kLane / VE; ++j) {
+            const int t = base + (j * 64 + lane) * VE;
+            if (t + VE <= a.vocab) {
+                u32x4 raw;
+                __builtin_memcpy(&raw, l + t, 16);  // (rows may start at any element)
+                unpack16<T>(raw, v + j * VE);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VE; ++i) v[j * VE + i] = t + i < a.vocab ? (float)l[t + i] : -inf;
+            }
         }
-        if ((tid & 63) == 0) sv[wave] = bv, si[wave] = bi;
-        __syncthreads();
-        for (int w = 0; w < 4; ++w)
-            if (before(sv[w], si[w], bv, bi)) bv = sv[w], bi = si[w];
-        __syncthreads();
-        if (k == 0) top = bv;
-        pv = bv;
-        pi = bi;
-        if (tid == 0) {
-            cand[k].logit = bv;
-            cand[k].token = bi == INT_MAX ? -1 : bi;
+        float m = -inf;
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            v[e] = v[e] > -inf ? __builtin_fminf(v[e], FLT_MAX) : -inf;  // (NaN becomes -inf)
+            m = __builtin_fmaxf(m, v[e]);
+        }
+        // the bound: the have-th best so far where there are W, and the W-th largest lane maximum
+        uint32_t bound = 0;
+        float block_top = -inf;
+        {
+            uint32_t rest = ascending(m);
+            for (int i = 0; i < W; ++i) {
+                bound = wave_max(rest);
+                if (i == 0) block_top = from_ascending(bound);
+                const uint64_t at = __ballot(rest == bound);
+                if (lane == __ffsll((unsigned long long)at) - 1) rest = 0;
+            }
+            if (have == W) {
+                const uint32_t old = __builtin_amdgcn_readlane((int)(mine >> 32), W - 1);
+                bound = old > bound ? old : bound;
+            }
+        }
+        if (block_top > -inf) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kLane; ++e)
+                s += __builtin_amdgcn_exp2f((v[e] - block_top) * 1.44269504f);
+            s = wave_sum(s);
+            const float now = __builtin_fmaxf(top, block_top);
+            sum = sum * __builtin_amdgcn_exp2f((top - now) * 1.44269504f) +
+                  s * __builtin_amdgcn_exp2f((block_top - now) * 1.44269504f);
+            top = now;
+        }
+        const float reach = from_ascending(bound);
+        auto token = [&](int e) { return base + ((e / VE) * 64 + lane) * VE + e % VE; };
+        if (lane < have) pool[wave][lane] = mine;
+        int n = have;
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            const bool in = v[e] >= reach;
+            const uint64_t who = __ballot(in);
+            if (who) {
+                const int at = n + __builtin_amdgcn_mbcnt_hi(
+                                       (uint32_t)(who >> 32),
+                                       __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+                if (in && at < 64) pool[wave][at] = make_key(v[e], token(e));
+                n += __popcll(who);
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (n <= 64) {
+            const Key k = lane < n ? pool[wave][lane] : 0;
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += pool[wave][j] > k;
+            have = n < W ? n : W;
+            if (lane < n && rank < W) best[wave][rank] = k;
+            __builtin_amdgcn_wave_barrier();
+            mine = lane < have ? best[wave][lane] : 0;
+        } else {
+            Key last = ~(Key)0, next = 0;
+            for (int r = 0; r < W; ++r) {
+                Key k = mine < last ? mine : 0;
+#pragma unroll
+                for (int e = 0; e < kLane; ++e) {
+                    const Key c = make_key(v[e], token(e));
+                    if (c < last && c > k) k = c;
+                }
+                last = wave_max(k);
+                if (lane == r) next = last;
+            }
+            mine = next;
+            have = W;
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+    char* out = (char*)a.ws + id * split_bytes(W);
+    if (lane == 0) *(SplitHead*)out = SplitHead{top, sum};
+    // (tokens behind the vocabulary are no tokens)
+    if (lane < W) ((Key*)(out + sizeof(SplitHead)))[lane] =
+        lane < have && key_token(mine) < a.vocab ? mine : 0;
+}
+
+// One workgroup per request.  A wave per beam (in turn): the splits' sums give the row's
+// log-sum-exp, and lane s walks split s's best tokens while the best head of all lanes is taken
+// W times.  Then the first wave does the same over the beams, on scores in 64 bits.
+__global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits) {
+    __shared__ Key rowbest[32][32];
+    __shared__ double rowlse[32];
+    constexpr int AHEAD = 4;  // of a split's tokens, loaded at once
+    const int r = blockIdx.x, lane = threadIdx.x & 63, W = a.beams;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const float inf = __builtin_inff();
+    const long long size = split_bytes(W);
+    for (int w = wave; w < W; w += blockDim.x / 64) {
+        const char* in = (const char*)a.ws + ((long long)(r * W + w) * splits + lane) * size;
+        const Key* keys = (const Key*)(in + sizeof(SplitHead));
+        const bool live = lane < splits;
+        SplitHead head = {-inf, 0.0f};
+        Key ahead[AHEAD];
+        if (live) head = *(const SplitHead*)in;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) ahead[i] = live && i < W ? keys[i] : 0;
+        const float top = from_ascending(wave_max(ascending(head.top)));
+        double part = 0.0;
+        if (head.top > -inf) part = (double)head.sum * exp((double)head.top - (double)top);
+        part = wave_sum(part);
+        if (lane == 0) rowlse[w] = top > -inf ? (double)top + log(part) : -(double)inf;
+        int at = 0;
+        Key cur = ahead[0];
+        for (int i = 0; i < W; ++i) {
+            const Key k = wave_max(cur);
+            if (lane == 0) rowbest[w][i] = k;
+            if (cur == k && k != 0) {
+                ++at;
+                Key next = 0;
+                if (at < W) {
+                    next = at >= AHEAD ? keys[at] : ahead[AHEAD - 1];
+#pragma unroll
+                    for (int q = 1; q < AHEAD - 1; ++q)
+                        if (at == q) next = ahead[q];
+                }
+                cur = next;
+            }
         }
     }
-    double sum = 0.0;
-    if (top > -__builtin_inff())
-        for (int v = tid; v < a.vocab; v += 256)
-            sum += (double)__builtin_amdgcn_exp2f((clean(l[v]) - top) * 1.44269504f);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-    if ((tid & 63) == 0) sd[wave] = sum;
     __syncthreads();
-    if (tid == 0) ((RowHead*)out)->lse = (double)top + log(sd[0] + sd[1] + sd[2] + sd[3]);
-}
-
-// One wave per request: lane w walks beam w's best tokens, and the best head of all lanes is
-// taken `beams` times.
-__global__ __launch_bounds__(64) void beam_merge_kernel(BeamArgs a) {
-    const int r = blockIdx.x, w = threadIdx.x;
-    const bool live = w < a.beams;
-    const int row = r * a.beams + (live ? w : 0);
-    const char* in = (const char*)a.ws + row * row_bytes(a.beams);
-    const Cand* cand = (const Cand*)(in + sizeof(RowHead));
-    const double lse = ((const RowHead*)in)->lse;
+    if (wave != 0) return;
+    const bool live = lane < W;
+    const int row = r * W + (live ? lane : 0);
+    const double lse = rowlse[live ? lane : 0];
     const float score = a.scores[row];
     const int ended = a.done ? a.done[row] : 0;
-    const float inf = __builtin_inff();
     const bool dead = !(score > -inf) || !(lse > -(double)inf);
     int at = 0;  // tokens of this beam taken so far
-    for (int k = 0; k < a.beams; ++k) {
+    for (int k = 0; k < W; ++k) {
         double total = -(double)inf;
-        int flat = INT_MAX;
-        if (live) {
-            int tok = -1;
+        int tok = -1;
+        if (live && at < W) {
             if (ended != 0 && score > -inf) {
                 // eos, then the other tokens in order
                 if (at == 0) {
@@ -115,26 +259,25 @@ __global__ __launch_bounds__(64) void beam_merge_kernel(BeamArgs a) {
             } else if (dead) {
                 tok = at < a.vocab ? at : -1;
             } else {
-                tok = cand[at].token;
-                const float l = cand[at].logit;
+                const Key c = rowbest[lane][at];
+                tok = c != 0 ? key_token(c) : -1;
+                const float l = key_logit(c);
                 if (tok >= 0 && l > -inf) total = (double)score + ((double)l - lse);
             }
-            if (tok >= 0) flat = w * a.vocab + tok;
         }
-        double bt = total;
-        int bf = flat;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const double t = __shfl_xor(bt, o);
-            const int f = __shfl_xor(bf, o);
-            if (t > bt || (t == bt && f < bf)) bt = t, bf = f;
-        }
-        if (live && flat == bf) {
-            const int i = r * a.beams + k;
-            a.next_scores[i] = (float)bt;
-            a.parent[i] = w;
-            a.token[i] = bf - w * a.vocab;
-            if (a.next_done) a.next_done[i] = ended != 0 || bf - w * a.vocab == a.eos;
+        // the largest total, then the lowest place in beams x vocabulary
+        const uint32_t low = ~(uint32_t)(lane * a.vocab + tok);
+        uint64_t u = __builtin_bit_cast(uint64_t, total + 0.0);
+        u ^= u >> 63 ? ~(uint64_t)0 : (uint64_t)1 << 63;
+        if (tok < 0) u = 0;
+        const Key first = wave_max((Key)u);
+        const uint32_t place = wave_max(u == first && tok >= 0 ? low : 0u);
+        if (tok >= 0 && u == first && low == place) {
+            const int i = r * W + k;
+            a.next_scores[i] = (float)total;
+            a.parent[i] = lane;
+            a.token[i] = tok;
+            if (a.next_done) a.next_done[i] = ended != 0 || tok == a.eos;
             ++at;
         }
     }
@@ -198,21 +341,23 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, int ch
 }  // namespace
 
 long long beam_workspace_bytes(const fcm_beam_problem& p) {
-    return (long long)p.requests * p.beams * row_bytes(p.beams);
+    return (long long)p.requests * p.beams * row_splits(p.vocab) * split_bytes(p.beams);
 }
 
 int launch_beam_select(const BeamArgs& a, int dtype, void* stream) {
     hipStream_t s = (hipStream_t)stream;
-    const int rows = a.requests * a.beams;
+    const int splits = row_splits(a.vocab), blocks = split_blocks(a.vocab);
+    const long long waves = (long long)a.requests * a.beams * splits;
+    const int grid = (int)((waves + 3) / 4);
     if (dtype == FCM_F32)
-        beam_rows_kernel<float><<<rows, 256, 0, s>>>(a);
+        beam_rows_kernel<float><<<grid, 256, 0, s>>>(a, splits, blocks);
     else if (dtype == FCM_F16)
-        beam_rows_kernel<_Float16><<<rows, 256, 0, s>>>(a);
+        beam_rows_kernel<_Float16><<<grid, 256, 0, s>>>(a, splits, blocks);
     else
-        beam_rows_kernel<__bf16><<<rows, 256, 0, s>>>(a);
+        beam_rows_kernel<__bf16><<<grid, 256, 0, s>>>(a, splits, blocks);
     const int rc = (int)hipGetLastError();
     if (rc != 0) return rc;
-    beam_merge_kernel<<<a.requests, 64, 0, s>>>(a);
+    beam_merge_kernel<<<a.requests, 64 * (a.beams < 8 ? a.beams : 8), 0, s>>>(a, splits);
     return (int)hipGetLastError();
 }
 
