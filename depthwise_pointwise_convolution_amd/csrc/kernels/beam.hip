@@ -56,7 +56,7 @@ __device__ __forceinline__ V wave_sum(V v) {
 
 // A wave looks at kBlock tokens of a row at a time, kLane of them in a lane's registers; one
 // wave's tokens are a split, of which a row has at most 64.
-constexpr int kLane = 32;
+constexpr int kLane = 16;
 constexpr int kBlock = 64 * kLane;
 // What selection keeps of a split: its largest logit, the sum of exp(logit - largest), and its
 // best tokens as keys, best first.
@@ -80,7 +80,7 @@ __host__ __device__ inline int row_splits(int vocab) {
 // dozen or so, gathered through LDS and ranked against each other.  Where many tokens are equal
 // (a masked row, coarse logits) more than 64 may reach it; then the best are taken one by one.
 template <typename T>
-__global__ __launch_bounds__(256) void beam_rows_kernel(BeamArgs a, int splits, int blocks) {
+__global__ __launch_bounds__(256, 8) void beam_rows_kernel(BeamArgs a, int splits, int blocks) {
     __shared__ Key pool[4][64], best[4][32];
     constexpr int VE = Vec<T>::N;
     const float inf = __builtin_inff();
@@ -202,6 +202,9 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const float inf = __builtin_inff();
     const long long size = split_bytes(W);
+    const int row = r * W + (lane < W ? lane : 0);  // of the first wave, at the end
+    const float score = a.scores[row];
+    const int ended = a.done ? a.done[row] : 0;
     for (int w = wave; w < W; w += blockDim.x / 64) {
         const char* in = (const char*)a.ws + ((long long)(r * W + w) * splits + lane) * size;
         const Key* keys = (const Key*)(in + sizeof(SplitHead));
@@ -237,10 +240,7 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits)
     __syncthreads();
     if (wave != 0) return;
     const bool live = lane < W;
-    const int row = r * W + (live ? lane : 0);
     const double lse = rowlse[live ? lane : 0];
-    const float score = a.scores[row];
-    const int ended = a.done ? a.done[row] : 0;
     const bool dead = !(score > -inf) || !(lse > -(double)inf);
     int at = 0;  // tokens of this beam taken so far
     for (int k = 0; k < W; ++k) {
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits)
     }
 }
 
-constexpr long long kChunk = 32768;  // bytes of a pool one workgroup copies
+constexpr long long kChunk = 16384;  // bytes of a pool one workgroup copies
 
 // Workgroups (beam, chunk): the beam's place among its parent's children says whether it keeps
 // the parent's slot (nothing to copy) or takes a freed one.  Slots that are read from belong to
@@ -327,7 +327,16 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, int ch
         const char* from = a.pool[q] + src * a.bytes[q];
         char* to = a.pool[q] + dst * a.bytes[q];
         const long long end = at + kChunk < a.bytes[q] ? at + kChunk : a.bytes[q];
-        if ((a.bytes[q] & 15) == 0 && ((uintptr_t)a.pool[q] & 15) == 0) {
+        const bool wide = (a.bytes[q] & 15) == 0 && ((uintptr_t)a.pool[q] & 15) == 0;
+        if (wide && end - at == kChunk) {
+            // a whole chunk: all of its loads in flight before the first store
+            constexpr int N = kChunk / (256 * 16);
+            u32x4 v[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = ld16(from + at + (i * 256 + threadIdx.x) * 16);
+#pragma unroll
+            for (int i = 0; i < N; ++i) st16(to + at + (i * 256 + threadIdx.x) * 16, v[i]);
+        } else if (wide) {
             for (long long i = at + threadIdx.x * 16; i < end; i += 256 * 16)
                 st16(to + i, ld16(from + i));
         } else {
