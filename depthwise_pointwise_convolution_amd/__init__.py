@@ -130,6 +130,7 @@ class fcm_beam_problem(ctypes.Structure):
 
 
 FCM_BEAM_POOLS = 8
+_POINTERS, _SIZES = ctypes.c_void_p * FCM_BEAM_POOLS, _i64 * FCM_BEAM_POOLS
 
 # every symbol include/fcm.h declares
 EXPORTS = ("fcm_dw1d_fwd", "fcm_dw1d_step", "fcm_scan_workspace", "fcm_scan_fwd",
@@ -557,8 +558,12 @@ def fcm_beam_select(prob, logits, scores, done, workspace, next_scores, parent, 
 def fcm_beam_reorder(prob, parent, slots, next_slots, pools, stream=None):
     """pools: state tensors whose first axis counts slots (contiguous)."""
     n = len(pools)
-    ptrs = (ctypes.c_void_p * n)(*[_ptr(t) for t in pools])
-    bytes_ = (_i64 * n)(*[t.stride(0) * t.element_size() for t in pools])
-    slots_ = (_i64 * n)(*[t.shape[0] for t in pools])
+    ptrs, bytes_, slots_ = _POINTERS(), _SIZES(), _SIZES()
+    if n > FCM_BEAM_POOLS:
+        raise ValueError("at most %d pools" % FCM_BEAM_POOLS)
+    for i, t in enumerate(pools):
+        ptrs[i] = t.data_ptr()
+        bytes_[i] = t.stride(0) * t.element_size()
+        slots_[i] = t.shape[0]
     _check(lib().fcm_beam_reorder(prob, _ptr(parent), _ptr(slots), _ptr(next_slots), n, ptrs,
                                   bytes_, slots_, _stream(stream)), "fcm_beam_reorder")

@@ -328,6 +328,71 @@ __global__ __launch_bounds__(64) void scan_step_kernel(ScanArgs a, int cblocks, 
     }
 }
 
+// The same with Q neighbouring lanes a channel, four states a lane, so that a wave's state is one
+// run of 16-byte pieces; the lanes' parts of the output are added among them.  A thread takes ROWS
+// rows of the batch, all their loads in flight at once, and reads A once for them.  The state's
+// bytes, read and written, bound it.
+template <typename T, int Q, int ROWS>
+__global__ __launch_bounds__(256) void scan_step4_kernel(ScanArgs a, int cblocks) {
+    constexpr int CH = 256 / Q;  // channels of a workgroup
+    const T *x = (const T*)a.x, *dt = (const T*)a.dt, *z = (const T*)a.z;
+    T* y = (T*)a.y;
+    const int row0 = blockIdx.x / cblocks * ROWS;
+    const int d0 = blockIdx.x % cblocks * CH + threadIdx.x / Q;
+    const int n = threadIdx.x % Q * 4;
+    const bool live = d0 < a.D;
+    const bool mine = live && n < a.N;  // (N need not fill the Q lanes)
+    const int d = live ? d0 : 0, nn = mine ? n : 0;
+    const long long bc = (long long)(d / (a.D / a.groups)) * a.N + nn;
+    float* st[ROWS];
+    f32x4 h[ROWS];
+    T xs[ROWS], ds[ROWS], zs[ROWS], B[ROWS][4], C[ROWS][4];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const long long row = row0 + i < a.seqs ? row0 + i : a.seqs - 1;
+        const int slot = seq_slot(a.slots, (int)row, a.nslots);
+        st[i] = slot >= 0 && row0 + i < a.seqs
+                    ? a.state + ((long long)slot * a.D + d) * a.N + nn : nullptr;
+        if (st[i]) h[i] = *(const f32x4*)st[i];
+        xs[i] = x[row * a.ldx + d];
+        ds[i] = dt[row * a.lddt + d];
+        if (z) zs[i] = z[row * a.ldz + d];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            B[i][j] = ((const T*)a.Bm)[row * a.ldb + bc + j];
+            C[i][j] = ((const T*)a.Cm)[row * a.ldc + bc + j];
+        }
+    }
+    f32x4 A = *(const f32x4*)(a.A + (long long)d * a.N + nn) * kLog2e;
+    const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f;
+    const float skip = a.skip ? a.skip[d] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        if (row0 + i >= a.seqs) break;
+        float out = 0.0f;
+        if (st[i]) {
+            const float xv = (float)xs[i];
+            float delta = (float)ds[i] + bias;
+            if (a.softplus) delta = softplus(delta);
+            const float dx = delta * xv;
+            if (mine) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    h[i][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A[j]), h[i][j],
+                                             dx * (float)B[i][j]);
+                    out = __builtin_fmaf((float)C[i][j], h[i][j], out);
+                }
+                *(f32x4*)st[i] = h[i];
+            }
+#pragma unroll
+            for (int o = 1; o < Q; o <<= 1) out += __shfl_xor(out, o);
+            out = __builtin_fmaf(skip, xv, out);
+            if (z) out *= silu((float)zs[i]);
+        }
+        if (live && n == 0) y[(row0 + i) * a.ldy + d] = (T)out;
+    }
+}
+
 // Tokens of a chunk.  One wave scans 64 channels of a chunk, and the card's 1024 SIMDs want about
 // four of them each to hide memory and instruction latency; a shorter chunk than that only costs
 // more starts to hand on, and one that holds the longest sequence possible spares the first pass.
@@ -372,16 +437,40 @@ int fwd_states(const ScanArgs& a, hipStream_t s) {
     return run_fwd<T, 64>(a, s);
 }
 
-template <typename T>
-int step_states(const ScanArgs& a, hipStream_t s) {
+template <typename T, int Q>
+int run_step4(const ScanArgs& a, hipStream_t s) {
+    const int cblocks = (a.D + 256 / Q - 1) / (256 / Q);
+    // Rows of a thread: 256 x 4096 channels of 16 states take 29.5 / 27.4 / 30 us with 1 / 2 / 4;
+    // one while the batch does not fill the card.
+    if ((long long)a.seqs * cblocks >= 4096) {
+        scan_step4_kernel<T, Q, 2><<<(a.seqs + 1) / 2 * cblocks, 256, 0, s>>>(a, cblocks);
+    } else {
+        scan_step4_kernel<T, Q, 1><<<a.seqs * cblocks, 256, 0, s>>>(a, cblocks);
+    }
+    return (int)hipGetLastError();
+}
+
+template <typename T, int NP>
+int run_step1(const ScanArgs& a, hipStream_t s) {
     const int cblocks = (a.D + 63) / 64;
     const long long units = (long long)a.seqs * cblocks;
-    const int grid = grid_of(units);
-    if (a.N <= 8) scan_step_kernel<T, 8><<<grid, 64, 0, s>>>(a, cblocks, units);
-    else if (a.N <= 16) scan_step_kernel<T, 16><<<grid, 64, 0, s>>>(a, cblocks, units);
-    else if (a.N <= 32) scan_step_kernel<T, 32><<<grid, 64, 0, s>>>(a, cblocks, units);
-    else scan_step_kernel<T, 64><<<grid, 64, 0, s>>>(a, cblocks, units);
+    scan_step_kernel<T, NP><<<grid_of(units), 64, 0, s>>>(a, cblocks, units);
     return (int)hipGetLastError();
+}
+
+template <typename T>
+int step_states(const ScanArgs& a, hipStream_t s) {
+    if (a.N % 4 == 0 && (((uintptr_t)a.A | (uintptr_t)a.state) & 15) == 0) {
+        if (a.N <= 4) return run_step4<T, 1>(a, s);
+        if (a.N <= 8) return run_step4<T, 2>(a, s);
+        if (a.N <= 16) return run_step4<T, 4>(a, s);
+        if (a.N <= 32) return run_step4<T, 8>(a, s);
+        return run_step4<T, 16>(a, s);
+    }
+    if (a.N <= 8) return run_step1<T, 8>(a, s);
+    if (a.N <= 16) return run_step1<T, 16>(a, s);
+    if (a.N <= 32) return run_step1<T, 32>(a, s);
+    return run_step1<T, 64>(a, s);
 }
 
 }  // namespace
