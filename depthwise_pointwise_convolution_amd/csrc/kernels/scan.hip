@@ -84,14 +84,26 @@ __device__ __forceinline__ bool find_chunk(const ScanArgs& a, int len, int c, Ch
 constexpr int kTurn = 4;
 constexpr int kScanWaves = 4;  // waves of a workgroup, 64 channels each
 
-// Tokens whose B and C a workgroup holds in LDS at a time: 16 KB of fp32.
-template <int NP>
+// Tokens whose B and C a workgroup holds in LDS at a time: 16 KB of fp32 for NS states.
+template <int NS>
 constexpr int scan_tile() {
-    return 16384 / (2 * NP * 4) / kTurn * kTurn;
+    return 16384 / (2 * NS * 4) / kTurn * kTurn;
 }
 
-// The scan of one chunk, in one of two passes.  A thread has one channel and its N states in
-// registers.  A sequence longer than a chunk is scanned twice, so that its chunks run at the same
+// Sum over the Q neighbouring lanes of a channel.
+template <int Q>
+__device__ __forceinline__ float quad_sum(float v) {
+    if constexpr (Q > 1)  // lanes 1 0 3 2
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                           0, __builtin_bit_cast(int, v), 0xb1, 0xf, 0xf, true));
+    if constexpr (Q > 2)  // lanes 2 3 0 1
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                           0, __builtin_bit_cast(int, v), 0x4e, 0xf, 0xf, true));
+    return v;
+}
+
+// The scan of one chunk, in one of two passes.  Q neighbouring lanes have one channel, NP of its
+// N states each, in registers.  A sequence longer than a chunk is scanned twice, so that its chunks run at the same
 // time: LAST = false finds what a chunk adds to a state (from zero; the first chunk from the
 // sequence's own) and the sum of its steps, whose exponential is the chunk's whole decay;
 // scan_join_kernel adds up where every chunk starts; LAST = true starts there and gives outputs
@@ -99,12 +111,11 @@ constexpr int scan_tile() {
 //
 // B and C are the same for all channels of a group: the workgroup converts them to fp32 in LDS
 // once a tile, and its lanes read them by broadcast, four states an instruction.
-template <typename T, int NP, bool LAST>
+template <typename T, int NP, int Q, bool LAST, bool GATE>
 __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a, int len, int chunks,
                                                                    int gblocks, bool wide) {
-    constexpr int TILE = scan_tile<NP>();
-    __shared__ f32x4 bc[TILE][(LAST ? 2 : 1) * NP / 4];
-    const bool gate = LAST && a.z != nullptr;
+    constexpr int NS = NP * Q, TILE = scan_tile<NS>();
+    __shared__ f32x4 bc[TILE][(LAST ? 2 : 1) * NS / 4];
     const int per = a.D / a.groups;
     const int cblocks = gblocks * a.groups;
     float* starts = (float*)a.ws;
@@ -116,13 +127,16 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a
     if (!LAST && k.index == k.count - 1) return;
     // channel blocks of one group: B and C are the same for the whole workgroup
     const int g = cb / gblocks;
-    const int dg = (cb % gblocks) * blockDim.x + threadIdx.x;
+    const int dg = ((cb % gblocks) * blockDim.x + threadIdx.x) / Q;
     const bool live = dg < per;
     const int d = g * per + (live ? dg : 0);
+    // this lane's states: [n0, n0 + left) of the channel's
+    const int n0 = threadIdx.x % Q * NP;
+    const int left = a.N - n0 < NP ? a.N - n0 : NP;
     // Row pointers, the same for the whole wave; they stay on the last row once they are there.
     const T* px = (const T*)a.x + k.first * a.ldx;
     const T* pd = (const T*)a.dt + k.first * a.lddt;
-    const T* pz = gate ? (const T*)a.z + k.first * a.ldz : nullptr;
+    const T* pz = (const T*)a.z + (GATE ? k.first * a.ldz : 0);
     T* py = (T*)a.y + k.first * a.ldy;
     T xs[kTurn], ds[kTurn], zs[kTurn];
     auto fetch = [&](int t, T* xv, T* dv, T* zv) {
@@ -130,19 +144,19 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a
         for (int i = 0; i < kTurn; ++i) {
             xv[i] = px[d];
             dv[i] = pd[d];
-            if (gate) zv[i] = pz[d];
+            if (GATE) zv[i] = pz[d];
             const bool more = t + i + 1 < k.end;
             px += more ? a.ldx : 0;
             pd += more ? a.lddt : 0;
-            if (gate) pz += more ? a.ldz : 0;
+            if (GATE) pz += more ? a.ldz : 0;
         }
     };
     if (k.first < k.end) fetch(k.first, xs, ds, zs);
     const int slot = a.state ? seq_slot(a.slots, k.seq, a.nslots) : -1;
-    float* st = slot >= 0 ? a.state + ((long long)slot * a.D + d) * a.N : nullptr;
+    float* st = slot >= 0 ? a.state + ((long long)slot * a.D + d) * a.N + n0 : nullptr;
     const bool carried = st && a.carry && a.carry[k.seq] != 0;
     float h[NP], A[NP];
-    load_states<NP>(a.A + (long long)d * a.N, a.N, wide, A);
+    load_states<NP>(a.A + (long long)d * a.N + n0, left, wide, A);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
         A[n] *= kLog2e;
@@ -152,53 +166,53 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a
     if (LAST && k.count > 1) {
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-            if (n < a.N) h[n] = starts[((long long)c * a.N + n) * a.D + d];
+            if (n < left) h[n] = starts[((long long)c * a.N + n0 + n) * a.D + d];
     } else if (k.index == 0 && carried) {
-        load_states<NP>(st, a.N, wide, h);
+        load_states<NP>(st, left, wide, h);
     }
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f;
     const float skip = LAST && a.skip ? a.skip[d] : 0.0f;
     if (!LAST && k.index == 0 && live) {
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-            if (n < a.N) starts[((long long)c * a.N + n) * a.D + d] = h[n];
+            if (n < left) starts[((long long)c * a.N + n0 + n) * a.D + d] = h[n];
     }
     float sum = 0.0f;
     for (int tile = k.first; tile < k.end; tile += TILE) {
         const int rows = tile + TILE < k.end ? TILE : k.end - tile;
         __syncthreads();
-        for (int i = threadIdx.x; i < rows * NP; i += blockDim.x) {
-            const int t = i / NP, n = i % NP;
+        for (int i = threadIdx.x; i < rows * NS; i += blockDim.x) {
+            const int t = i / NS, n = i % NS;
             const long long r = tile + t;
             const bool in = n < a.N;
             const T* b = (const T*)a.Bm + r * a.ldb + (long long)g * a.N + n;
             const T* cc = (const T*)a.Cm + r * a.ldc + (long long)g * a.N + n;
             float* to = (float*)bc[t];
             to[n] = in ? (float)*b : 0.0f;
-            if (LAST) to[NP + n] = in ? (float)*cc : 0.0f;
+            if (LAST) to[NS + n] = in ? (float)*cc : 0.0f;
         }
         __syncthreads();
         for (int t0 = 0; t0 < rows; t0 += kTurn) {
             T xn[kTurn], dn[kTurn], zn[kTurn];
             fetch(tile + t0 + kTurn, xn, dn, zn);
+            float outs[kTurn];
 #pragma unroll
             for (int i = 0; i < kTurn; ++i) {
                 // Tokens behind the end take a step of zero, which leaves the state as it is
-                // (their row of the tile is an old one, or the last).
+                // (their row of the tile is the last).
                 const bool here = t0 + i < rows;
-                const f32x4* row = bc[here ? t0 + i : rows - 1];
+                const f32x4* row = bc[here ? t0 + i : rows - 1] + n0 / 4;
                 const float xv = (float)xs[i];
                 const float v = (float)ds[i] + bias;
                 const float sp = softplus(v);
-                float delta = a.softplus ? sp : v;
-                delta = here ? delta : 0.0f;
+                const float delta = here ? (a.softplus ? sp : v) : 0.0f;
                 const float dx = here ? delta * xv : 0.0f;
-                float out = skip * xv;
+                float out = 0.0f;
 #pragma unroll
                 for (int q = 0; q < NP / 4; ++q) {
                     const f32x4 B = row[q];
                     f32x4 C;
-                    if (LAST) C = row[NP / 4 + q];
+                    if (LAST) C = row[NS / 4 + q];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int n = 4 * q + j;
@@ -208,12 +222,23 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a
                     }
                 }
                 if (LAST) {
-                    if (gate) out *= silu((float)zs[i]);
-                    if (here && live) py[d] = (T)out;
-                    py += a.ldy;
+                    out = __builtin_fmaf(skip, xv, quad_sum<Q>(out));
+                    outs[i] = GATE ? out * silu((float)zs[i]) : out;
+                    // Few states a lane: the turn's tokens are one block of straight code, whose
+                    // chains overlap, and are stored behind it.  With many states their operands
+                    // would not fit in the registers: the store ends each token's block.
+                    if (NP >= 8 && here && live && n0 == 0) (py + i * a.ldy)[d] = (T)outs[i];
                 } else {
                     sum += delta;
                 }
+            }
+            if (LAST) {
+                if (NP < 8) {
+#pragma unroll
+                    for (int i = 0; i < kTurn; ++i)
+                        if (t0 + i < rows && live && n0 == 0) (py + i * a.ldy)[d] = (T)outs[i];
+                }
+                py += kTurn * a.ldy;
             }
 #pragma unroll
             for (int i = 0; i < kTurn; ++i) xs[i] = xn[i], ds[i] = dn[i], zs[i] = zn[i];
@@ -221,12 +246,12 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a
     }
     if (!live) return;
     if (LAST) {
-        if (st && k.index == k.count - 1) store_states<NP>(st, a.N, wide, h);
+        if (st && k.index == k.count - 1) store_states<NP>(st, left, wide, h);
     } else if (c + 1 < chunks) {
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-            if (n < a.N) starts[((long long)(c + 1) * a.N + n) * a.D + d] = h[n];
-        sums[(long long)c * a.D + d] = sum;
+            if (n < left) starts[((long long)(c + 1) * a.N + n0 + n) * a.D + d] = h[n];
+        if (n0 == 0) sums[(long long)c * a.D + d] = sum;
     }
 }
 
@@ -393,48 +418,63 @@ __global__ __launch_bounds__(256) void scan_step4_kernel(ScanArgs a, int cblocks
     }
 }
 
-// Tokens of a chunk.  One wave scans 64 channels of a chunk, and the card's 1024 SIMDs want about
-// four of them each to hide memory and instruction latency; a shorter chunk than that only costs
-// more starts to hand on, and one that holds the longest sequence possible spares the first pass.
-int chunk_len(int tokens, int D, int groups) {
-    const long long cblocks = (long long)((D / groups + 63) / 64) * groups;
-    const long long want = tokens * cblocks / 8192;
-    int len = 32;
-    while ((len < want && len < 256) || tokens / len * cblocks > (1 << 25)) len *= 2;
+// Waves the scan would have if each took 64 channels of one token, in 4096ths.
+long long token_waves(int tokens, int D, int groups) {
+    return (long long)tokens * ((D / groups + 63) / 64) * groups / 4096;
+}
+
+// Tokens of a chunk: short ones bring waves for a small batch, long ones hand on fewer states.
+// us with 8 / 16 / 32 / 64 / 128 tokens, 16 states, bf16:
+//   512 x 1024: 27 / 29 / 38 / 59 / 102, 512 x 4096: 40 / 35 / 40 / 60 / 102,
+//   2048 x 2048: 76 / 59 / 54 / 65 / 107, 8192 x 4096: 425 / 291 / 237 / 221 / 232.
+// One thread goes along a sequence's chunks to join them, so a long sequence has no more than 256:
+// 16000 x 256 takes 87 us with 32 and 80 with 64.
+int chunk_len(int tokens, int seqs, int D, int groups) {
+    const long long w = token_waves(tokens, D, groups);
+    int len = w < 2 ? 8 : w < 12 ? 16 : w < 48 ? 32 : 64;
+    while (tokens / len > 256ll * (seqs > 0 ? seqs : 1) || tokens / len * (D / 64 + 1ll) > (1 << 24))
+        len *= 2;
     return len;
 }
 
 int grid_of(long long units) { return (int)(units < (1 << 22) ? units : (1 << 22)); }
 
-template <typename T, int NP>
+template <typename T, int NP, int Q>
 int run_fwd(const ScanArgs& a, hipStream_t s) {
-    const int len = chunk_len(a.tokens, a.D, a.groups);
+    const int len = chunk_len(a.tokens, a.seqs, a.D, a.groups);
     const int chunks = a.tokens / len + a.seqs;
-    const int waves = (a.D / a.groups + 63) / 64;
+    const int waves = (a.D / a.groups * Q + 63) / 64;
     const int block = 64 * (waves < kScanWaves ? waves : kScanWaves);
-    const int gblocks = (a.D / a.groups + block - 1) / block;
+    const int gblocks = (a.D / a.groups + block / Q - 1) / (block / Q);
     const int grid = chunks * gblocks * a.groups;
     const bool wide = a.N % 4 == 0 && (((uintptr_t)a.A | (uintptr_t)a.state) & 15) == 0;
     if (a.tokens > len) {
-        scan_fwd_kernel<T, NP, false><<<grid, block, 0, s>>>(a, len, chunks, gblocks, wide);
+        scan_fwd_kernel<T, NP, Q, false, false><<<grid, block, 0, s>>>(a, len, chunks, gblocks, wide);
         if (a.tokens > 2 * len) {
             const int blocks = (int)(((long long)a.N * a.D + 255) / 256);
             const long long joins = (long long)a.seqs * blocks;
             scan_join_kernel<<<grid_of(joins), 256, 0, s>>>(a, len, chunks, blocks, joins);
         }
     }
-    scan_fwd_kernel<T, NP, true><<<grid, block, 0, s>>>(a, len, chunks, gblocks, wide);
+    if (a.z)
+        scan_fwd_kernel<T, NP, Q, true, true><<<grid, block, 0, s>>>(a, len, chunks, gblocks, wide);
+    else
+        scan_fwd_kernel<T, NP, Q, true, false><<<grid, block, 0, s>>>(a, len, chunks, gblocks, wide);
     return (int)hipGetLastError();
 }
 
+// Lanes of a channel.  16 states a lane leave the least to do twice; more states than that are
+// spread over lanes, and so are those of a batch too small to give every SIMD a wave, whose time
+// is the chain of one wave: 300 x 64 channels of 16 states take 23 us on one lane, 18 on four.
 template <typename T>
 int fwd_states(const ScanArgs& a, hipStream_t s) {
-    if (a.N <= 8) return run_fwd<T, 8>(a, s);
-    if (a.N <= 16) return run_fwd<T, 16>(a, s);
-    if (a.N <= 24) return run_fwd<T, 24>(a, s);
-    if (a.N <= 32) return run_fwd<T, 32>(a, s);
-    if (a.N <= 48) return run_fwd<T, 48>(a, s);
-    return run_fwd<T, 64>(a, s);
+    const bool few = token_waves(a.tokens, a.D, a.groups) < 3;
+    if (a.N <= 8) return few ? run_fwd<T, 4, 2>(a, s) : run_fwd<T, 8, 1>(a, s);
+    if (a.N <= 16) return few ? run_fwd<T, 4, 4>(a, s) : run_fwd<T, 16, 1>(a, s);
+    if (a.N <= 24) return run_fwd<T, 12, 2>(a, s);
+    if (a.N <= 32) return run_fwd<T, 16, 2>(a, s);
+    if (a.N <= 48) return run_fwd<T, 12, 4>(a, s);
+    return run_fwd<T, 16, 4>(a, s);
 }
 
 template <typename T, int Q>
@@ -489,7 +529,7 @@ int launch_scan_step(const ScanArgs& a, int dtype, void* stream) {
 }
 long long scan_workspace_bytes(const fcm_scan_problem& p) {
     const int groups = p.groups > 0 ? p.groups : 1;
-    const int len = chunk_len(p.tokens, p.D, groups);
+    const int len = chunk_len(p.tokens, p.seqs, p.D, groups);
     if (p.tokens <= len) return 0;
     return (long long)(p.tokens / len + p.seqs) * p.D * (p.N + 1) * 4;
 }
