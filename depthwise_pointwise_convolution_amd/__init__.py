@@ -559,9 +559,7 @@ def fcm_beam_reorder(prob, parent, slots, next_slots, pools, stream=None):
     """pools: state tensors whose first axis counts slots (contiguous)."""
     n = len(pools)
     ptrs, bytes_, slots_ = _POINTERS(), _SIZES(), _SIZES()
-    if n > FCM_BEAM_POOLS:
-        raise ValueError("at most %d pools" % FCM_BEAM_POOLS)
-    for i, t in enumerate(pools):
+    for i, t in zip(range(FCM_BEAM_POOLS), pools):  # (more are refused below)
         ptrs[i] = t.data_ptr()
         bytes_[i] = t.stride(0) * t.element_size()
         slots_[i] = t.shape[0]

@@ -1,13 +1,19 @@
 // scan.hip -- selective state-space scan, for packed prompts and for one token of each
 // sequence.  Per channel d and state n:
 //   h = exp(delta * A) * h + delta * B * x,   y = (sum_n C * h + skip * x) * silu(z).
+#include <float.h>
+
 #include "seq_common.h"
 #include "../seq.h"
 
 namespace fcm {
 namespace {
 
-constexpr float kLog2e = 1.44269504f;
+// A in base 2.  A decay rate of -infinity is taken as the largest float: a step of zero then still
+// leaves the state alone (0 * infinity would be NaN).
+__device__ __forceinline__ float rate2(float A) {
+    return __builtin_fmaxf(A * 1.44269504f, -FLT_MAX);
+}
 
 // A channel's N <= NP values: in 16-byte pieces (`wide`: N is a multiple of 4 and the array 16-byte
 // aligned), or one by one.
@@ -159,7 +165,7 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a
     load_states<NP>(a.A + (long long)d * a.N + n0, left, wide, A);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-        A[n] *= kLog2e;
+        A[n] = rate2(A[n]);
         h[n] = 0.0f;
     }
     // (with several chunks the last one may already be writing the state)
@@ -286,7 +292,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a, int len, int
         const long long i = (u % blocks) * 256 + threadIdx.x;
         if (count <= 2 || i >= plane) continue;
         const int d = (int)(i % a.D);
-        const float A = a.A[(long long)d * a.N + i / a.D] * kLog2e;
+        const float A = rate2(a.A[(long long)d * a.N + i / a.D]);
         float* s = starts + (long long)before * plane + i;
         const float* w = sums + (long long)before * a.D + d;
         float add[kJoin], sum[kJoin];
@@ -340,7 +346,7 @@ __global__ __launch_bounds__(64) void scan_step_kernel(ScanArgs a, int cblocks, 
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
                 if (n < a.N) {
-                    const float A = a.A[(long long)d * a.N + n] * kLog2e;
+                    const float A = rate2(a.A[(long long)d * a.N + n]);
                     const float h = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A), st[n],
                                                    dx * (float)b[n]);
                     st[n] = h;
@@ -388,7 +394,9 @@ __global__ __launch_bounds__(256) void scan_step4_kernel(ScanArgs a, int cblocks
             C[i][j] = ((const T*)a.Cm)[row * a.ldc + bc + j];
         }
     }
-    f32x4 A = *(const f32x4*)(a.A + (long long)d * a.N + nn) * kLog2e;
+    f32x4 A = *(const f32x4*)(a.A + (long long)d * a.N + nn);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) A[j] = rate2(A[j]);
     const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f;
     const float skip = a.skip ? a.skip[d] : 0.0f;
 #pragma unroll

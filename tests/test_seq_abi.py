@@ -172,3 +172,45 @@ def test_sequence_sources_are_built():
     have = {s for s, _ in build.SOURCES}
     on_disk = {"kernels/" + f for f in os.listdir(os.path.join(build.CSRC, "kernels")) if f.endswith(".hip")}
     assert on_disk <= have
+
+
+# ------------------------------------------------------------------------------------------
+# the convenience wrappers' own checks, on the CPU
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("C,group,symmetric", [(64, 32, False), (200, 64, False), (136, 128, True), (32, 32, True)])
+def test_quantized_weights_are_within_half_a_step(C, group, symmetric):
+    import torch
+    from depthwise_pointwise_convolution_amd.sequence import Q4Linear, quantize_q4
+    g = torch.Generator().manual_seed(C)
+    w = (torch.randn(9, C, generator=g) * 0.1).to(torch.float16)
+    w[3] = 0
+    w[4] = w[4].abs()
+    q, scales, zeros = quantize_q4(w, group, symmetric)
+    back = Q4Linear(q, scales, zeros, group=group).weight()
+    step = scales.float()[:, torch.arange(C) // group]
+    # half a step, and where the rounded scale falls short of the span or the zero is rounded, up to
+    # 15 codes times the scale's rounding (2^-11), or another half step at the far end
+    assert ((back - w.float()).abs() <= step * (1.0 if not symmetric else 0.5) + step * 15 * 2.0 ** -11 + 1e-9).all()
+    assert (back[3] == 0).all()
+    assert (zeros is None) == symmetric
+
+
+def test_wrappers_refuse_wrong_shapes_and_types():
+    import torch
+    from depthwise_pointwise_convolution_amd.sequence import BeamSearch, Q4Linear, StateSpaceBlock, quantize_q4
+    z = torch.zeros
+    q, s = z(8, 32, dtype=torch.uint8), z(8, 1, dtype=torch.float16)
+    for bad in (lambda: quantize_q4(z(8, 64)), lambda: quantize_q4(z(8, 60, dtype=torch.float16)),
+                lambda: quantize_q4(z(8, 64, dtype=torch.float16), 16),
+                lambda: Q4Linear(q.int(), s), lambda: Q4Linear(q, s.float()), lambda: Q4Linear(q, s, group=32),
+                lambda: Q4Linear(q, s, zeros=z(8, 2, dtype=torch.uint8)), lambda: Q4Linear(q, s, bias=z(7)),
+                lambda: Q4Linear(q, s, act="gelu"), lambda: Q4Linear(q, s)(z(2, 63, dtype=torch.float16)),
+                lambda: Q4Linear(q, s)(z(2, 64)), lambda: Q4Linear(q, s)(z(64, 2, dtype=torch.float16).t()),
+                lambda: StateSpaceBlock(None, z(8, 4), None, None, None, None, z(7, 16), None, None, 1),
+                lambda: StateSpaceBlock(None, z(8, 4), z(7), None, None, None, z(8, 16), None, None, 1),
+                lambda: BeamSearch(2, 3, 10, z(5, dtype=torch.int32)),
+                lambda: BeamSearch(2, 3, 10, z(6)),
+                lambda: BeamSearch(1, 2, 10, z(2, dtype=torch.int32)).advance(z(2, 9), []),
+                lambda: BeamSearch(1, 2, 10, z(2, dtype=torch.int32)).advance(z(3, 10), [])):
+        with pytest.raises(ValueError):
+            bad()

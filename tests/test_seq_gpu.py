@@ -520,3 +520,81 @@ def test_results_do_not_depend_on_the_run():
     first = _run_scan(F, v, "f32", _offsets(lens), [0, 1], [1, 0], 1, (0, 0, 0, 0))
     again = _run_scan(F, v, "f32", _offsets(lens), [0, 1], [1, 0], 1, (0, 0, 0, 0))
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+# ------------------------------------------------------------------------------------------
+# offsets past 32 bits, and the operators together
+# ------------------------------------------------------------------------------------------
+def test_states_and_rows_past_32_bits():
+    import depthwise_pointwise_convolution_amd as F
+    g = _gen(6)
+    D, N, slots = 2048, 16, 70000  # a pool of 9 GB
+    assert slots * D * N * 4 > 2 ** 33
+    v = _scan_inputs(g, "bf16", 2, D, N, 1, 2, 2, True)
+    pool = torch.empty(slots, D, N, device="cuda")
+    where = [slots - 1, slots // 2 + 7]
+    pool[where] = v["state"].cuda()
+    small, big = dict(v), dict(v, state=None)
+    want, ws = _run_scan(F, small, "bf16", None, [0, 1], None, 1, (0, 0, 0, 0), step=True)
+    prob = F.scan_problem("bf16", D, N, tokens=2, seqs=2, slots=slots)
+    y = torch.empty(2, D, dtype=torch.bfloat16, device="cuda")
+    dev = [big[k].cuda() for k in ("x", "dt", "A", "Bm", "Cm", "skip", "dt_bias", "z")]
+    F.fcm_scan_step(prob, *dev, torch.tensor(where, dtype=torch.int32).cuda(), pool, y)
+    assert torch.equal(y, want) and torch.equal(pool[where], ws)
+    # beams over the same pool
+    prob = F.beam_problem("f32", 1, 2, 100)
+    parent = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out = torch.empty(2, dtype=torch.int32, device="cuda")
+    F.fcm_beam_reorder(prob, parent, torch.tensor(where, dtype=torch.int32).cuda(), out, [pool])
+    assert out.tolist() == where and torch.equal(pool[where[1]], pool[where[0]])
+    del pool
+    # rows that lie 2^31 bytes apart
+    T, ld = 4, 2 ** 30 + 64
+    wide = torch.empty(T * ld, dtype=torch.bfloat16, device="cuda").as_strided((T, 64), (ld, 1))
+    x = _normal(g, T, 64, dtype="bf16")
+    wide.copy_(x)
+    w = _normal(g, 64, 4, dtype="bf16")
+    prob = F.dw1d_problem("bf16", 64, 4, tokens=T, seqs=1, ldx=ld)
+    y = torch.empty(T, 64, dtype=torch.bfloat16, device="cuda")
+    F.fcm_dw1d_fwd(prob, wide, w.cuda(), None, torch.tensor([0, T], dtype=torch.int32).cuda(), None, None, None, y)
+    ref, tol, _, _ = O.dw1d("bf16", x, w, None, [0, T], [0], [0], None, True)
+    _within(y, ref, tol, "rows far apart")
+    logits, scores, _ = _beam_case(g, "bf16", 1, T, 64, -1)
+    wide.copy_(logits)
+    prob = F.beam_problem("bf16", 1, T, 64, ldl=ld)
+    out = [torch.empty(T, dtype=t, device="cuda") for t in (torch.float32,) + (torch.int32,) * 3]
+    F.fcm_beam_select(prob, wide, scores.cuda(), None,
+                      torch.empty(F.fcm_beam_workspace(prob), dtype=torch.uint8, device="cuda"), *out)
+    ref = O.beam(logits, scores, None, T, -1)
+    assert out[1].tolist() == ref[1].tolist() and out[2].tolist() == ref[2].tolist()
+
+
+def test_a_rate_of_minus_infinity_forgets_and_no_step_keeps():
+    import depthwise_pointwise_convolution_amd as F
+    g = _gen(9)
+    T, D, N = 6, 8, 16
+    v = _scan_inputs(g, "f32", T, D, N, 1, 1, 1, False)
+    v["A"][:, 0] = -math.inf
+    v["dt_bias"] = None
+    v["dt"] = v["dt"].abs()
+    y, state = _run_scan(F, v, "f32", [0, T], [0], [1], 1, (0, 0, 0, 0), softplus=False)
+    assert y.isfinite().all() and state.isfinite().all()
+    last = (v["dt"][-1] * v["x"][-1] * v["Bm"][-1, 0]).double()
+    _within(state[0, :, 0], last, 4 * O.U * last.abs(), "state that forgets")
+    v["dt"] = torch.zeros_like(v["dt"])
+    _, state = _run_scan(F, v, "f32", [0, T], [0], [1], 1, (0, 0, 0, 0), softplus=False)
+    assert torch.equal(state.cpu(), v["state"])
+
+
+def test_example_decodes_and_its_scores_hold():
+    # every beam's score, summed over single-token steps with reordered states, against one prompt
+    # run over the beam's tokens.  Both round activations to bf16 (2^-8) at some ten places a layer
+    # in different orders; logits are of order 1, so a token's log-probability moves by a few 2^-8
+    # and the sum over 12 tokens by well under 0.5 (a wrong state changes it by several units)
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import state_space_decode as E
+    worst = E.main(["--dim", "128", "--layers", "2", "--vocab", "501", "--requests", "3", "--beams", "4",
+                    "--tokens", "12", "--check"])
+    assert worst < 0.5
