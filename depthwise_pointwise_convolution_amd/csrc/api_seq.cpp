@@ -349,9 +349,8 @@ fcm_status fcm_beam_reorder(const fcm_beam_problem* prob, const int32_t* parent,
     memset(&a, 0, sizeof(a));
     for (int p = 0; p < npools; ++p) {
         if (!pools[p]) return invalid("a pool is NULL");
-        if (misaligned(pools[p], 4)) return invalid("a pool is not 4-byte aligned");
-        if (pool_bytes[p] < 4 || pool_bytes[p] % 4 != 0 || pool_bytes[p] > (1ll << 40))
-            return invalid("a slot's bytes must be a positive multiple of 4");
+        if (pool_bytes[p] < 1 || pool_bytes[p] > (1ll << 40))
+            return invalid("a slot's bytes must be 1 to 2^40");
         if (pool_slots[p] < 0) return invalid("pool_slots must not be negative");
         a.pool[p] = (char*)pools[p];
         a.bytes[p] = pool_bytes[p];

@@ -318,30 +318,34 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, int ch
     if (chunk == 0 && threadIdx.x == 0) a.next_slots[beam] = dst;
     long long at = chunk * kChunk;  // along the pools laid end to end, each rounded up to chunks
     for (int q = 0; q < a.npools; ++q) {
-        const long long whole = (a.bytes[q] + kChunk - 1) / kChunk * kChunk;
-        if (at >= whole) {
-            at -= whole;
+        const long long room = (a.bytes[q] + kChunk - 1) / kChunk * kChunk;
+        if (at >= room) {
+            at -= room;
             continue;
         }
         if (src < 0 || src >= a.nslots[q] || dst < 0 || dst >= a.nslots[q]) return;
         const char* from = a.pool[q] + src * a.bytes[q];
         char* to = a.pool[q] + dst * a.bytes[q];
         const long long end = at + kChunk < a.bytes[q] ? at + kChunk : a.bytes[q];
-        const bool wide = (a.bytes[q] & 15) == 0 && ((uintptr_t)a.pool[q] & 15) == 0;
-        if (wide && end - at == kChunk) {
+        // (slots may start at any byte: such 16-byte accesses are still one instruction)
+        if (end - at == kChunk) {
             // a whole chunk: all of its loads in flight before the first store
             constexpr int N = kChunk / (256 * 16);
             u32x4 v[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = ld16(from + at + (i * 256 + threadIdx.x) * 16);
+            for (int i = 0; i < N; ++i)
+                __builtin_memcpy(&v[i], from + at + (i * 256 + threadIdx.x) * 16, 16);
 #pragma unroll
-            for (int i = 0; i < N; ++i) st16(to + at + (i * 256 + threadIdx.x) * 16, v[i]);
-        } else if (wide) {
-            for (long long i = at + threadIdx.x * 16; i < end; i += 256 * 16)
-                st16(to + i, ld16(from + i));
+            for (int i = 0; i < N; ++i)
+                __builtin_memcpy(to + at + (i * 256 + threadIdx.x) * 16, &v[i], 16);
         } else {
-            for (long long i = at + threadIdx.x * 4; i < end; i += 256 * 4)
-                *(uint32_t*)(to + i) = *(const uint32_t*)(from + i);
+            const long long whole = at + (end - at) / 16 * 16;
+            for (long long i = at + threadIdx.x * 16; i < whole; i += 256 * 16) {
+                u32x4 v;
+                __builtin_memcpy(&v, from + i, 16);
+                __builtin_memcpy(to + i, &v, 16);
+            }
+            if (whole + threadIdx.x < end) to[whole + threadIdx.x] = from[whole + threadIdx.x];
         }
         return;
     }

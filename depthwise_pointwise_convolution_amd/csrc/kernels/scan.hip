@@ -57,10 +57,11 @@ __device__ __forceinline__ bool find_chunk(const ScanArgs& a, int len, int c, Ch
     int base = 0;
     for (int b0 = 0; b0 < a.seqs; b0 += 64) {
         const int b = b0 + lane;
-        int n = 0;
+        int n = 0, start = 0, end = 0;
         if (b < a.seqs) {
-            const int rows = seq_offset(a.cu, b + 1, a.tokens) - seq_offset(a.cu, b, a.tokens);
-            n = rows > len ? (rows + len - 1) / len : 1;
+            start = seq_offset(a.cu, b, a.tokens);
+            end = seq_offset(a.cu, b + 1, a.tokens);
+            n = end - start > len ? (end - start + len - 1) / len : 1;
         }
         int upto = n;  // chunks of sequences b0 .. b
 #pragma unroll
@@ -74,11 +75,9 @@ __device__ __forceinline__ bool find_chunk(const ScanArgs& a, int len, int c, Ch
             out->seq = b0 + k;
             out->count = __builtin_amdgcn_readlane(n, k);
             out->index = c - before;
-            // (scalar registers: every lane has the same)
-            const int start = __builtin_amdgcn_readfirstlane(seq_offset(a.cu, out->seq, a.tokens));
-            const int end = __builtin_amdgcn_readfirstlane(seq_offset(a.cu, out->seq + 1, a.tokens));
-            out->first = start + out->index * len;
-            out->end = out->first + len < end ? out->first + len : end;
+            out->first = __builtin_amdgcn_readlane(start, k) + out->index * len;
+            const int last = __builtin_amdgcn_readlane(end, k);
+            out->end = out->first + len < last ? out->first + len : last;
             return true;
         }
         base += __builtin_amdgcn_readlane(upto, 63);

@@ -545,10 +545,9 @@ fcm_status fcm_beam_select(const fcm_beam_problem* prob, const void* logits,
 /* Gives the next beams their states: next_slots[i] becomes a slot holding the state of
  * slots[parent of i].  Of the children of one beam the first keeps its slot; the others
  * take, in order, the slots of the beams without a child, and only those are copied, in
- * place: pool p is [..][pool_bytes[p]] with pool_slots[p] slots (pool_bytes a multiple of 4
- * and the pools 4-byte aligned; multiples of 16 take the wide copies).  slots, next_slots:
- * [requests*beams] int32, distinct arrays; the slots must be distinct.  A parent outside
- * [0, beams) counts as beam 0; a slot outside a pool is not copied from or to. */
+ * place: pool p is [pool_slots[p]][pool_bytes[p]] bytes, of any size and alignment.  slots,
+ * next_slots: [requests*beams] int32, distinct arrays; the slots must be distinct.  A parent
+ * outside [0, beams) counts as beam 0; a slot outside a pool is not copied from or to. */
 fcm_status fcm_beam_reorder(const fcm_beam_problem* prob, const int32_t* parent,
                             const int32_t* slots, int32_t* next_slots, int32_t npools,
                             void* const* pools, const int64_t* pool_bytes,

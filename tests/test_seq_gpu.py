@@ -436,6 +436,10 @@ def test_beam_reorder(W, shapes):
     slots = torch.randperm(n + 5, generator=g)[:n].to(torch.int32)
     pools = [torch.randn(n + 5, *s, generator=g) for s in shapes]
     pools.append(torch.randn(n + 5, 24, generator=g).to(torch.bfloat16))
+    # slots whose bytes are no multiple of a word, below and above what a workgroup copies
+    pools.append(torch.randn(n + 5, 8193, generator=g).to(torch.bfloat16))
+    pools.append(torch.randint(0, 256, (n + 5, 16403), generator=g, dtype=torch.uint8))
+    pools.append(torch.randint(0, 256, (n + 5, 7), generator=g, dtype=torch.uint8))
     want, wpools = O.reorder(parent.tolist(), slots.tolist(), W, pools)
     got = [p.cuda() for p in pools]
     out = torch.full((n,), -9, dtype=torch.int32, device="cuda")
