@@ -9,6 +9,9 @@
 namespace fcm {
 namespace {
 
+// 16 bytes from any address: one access like an aligned one.
+typedef u32x4 __attribute__((aligned(1))) u32x4_any;
+
 // Selection works on keys that order as integers: a float's bits turned so that they ascend, and
 // below them the complement of the token, so that among equal logits the lowest token is largest.
 // 0 is below every key.
@@ -101,9 +104,8 @@ __global__ __launch_bounds__(256, 8) void beam_rows_kernel(BeamArgs a, int split
         for (int j = 0; j < kLane / VE; ++j) {
             const int t = base + (j * 64 + lane) * VE;
             if (t + VE <= a.vocab) {
-                u32x4 raw;
-                __builtin_memcpy(&raw, l + t, 16);  // (rows may start at any element)
-                unpack16<T>(raw, v + j * VE);
+                // (rows may start at any element)
+                unpack16<T>(*(const u32x4_any*)(l + t), v + j * VE);
             } else {
 #pragma unroll
                 for (int i = 0; i < VE; ++i) v[j * VE + i] = t + i < a.vocab ? (float)l[t + i] : -inf;
@@ -334,17 +336,14 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(ReorderArgs a, int ch
             u32x4 v[N];
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                __builtin_memcpy(&v[i], from + at + (i * 256 + threadIdx.x) * 16, 16);
+                v[i] = *(const u32x4_any*)(from + at + (i * 256 + threadIdx.x) * 16);
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                __builtin_memcpy(to + at + (i * 256 + threadIdx.x) * 16, &v[i], 16);
+                *(u32x4_any*)(to + at + (i * 256 + threadIdx.x) * 16) = v[i];
         } else {
             const long long whole = at + (end - at) / 16 * 16;
-            for (long long i = at + threadIdx.x * 16; i < whole; i += 256 * 16) {
-                u32x4 v;
-                __builtin_memcpy(&v, from + i, 16);
-                __builtin_memcpy(to + i, &v, 16);
-            }
+            for (long long i = at + threadIdx.x * 16; i < whole; i += 256 * 16)
+                *(u32x4_any*)(to + i) = *(const u32x4_any*)(from + i);
             if (whole + threadIdx.x < end) to[whole + threadIdx.x] = from[whole + threadIdx.x];
         }
         return;
