@@ -1,5 +1,11 @@
 // beam.hip -- beam search: the best continuations of each request over beams and vocabulary,
 // and the reordering of the beams' states.
+//
+// Both are readings of memory.  On MI355X, 32 requests of 8 beams over 65537 fp32 logits: the rows
+// 25 us (67 MB, 2.7 TB/s: instruction issue, the vector units busy 45% of the time beside the waits
+// of the cross-lane steps; 16 or 32 tokens a lane, one block or several a wave take 25 to 29 us),
+// the merge 8.5 us (a chain of latencies), the copies of 158 states of 1.1 MB 52 us (7 TB/s, part of
+// it from the Infinity Cache).  One request of 4 beams over 32000 fp16 logits: 4.6, 5 and 4 us.
 #include <float.h>
 #include <limits.h>
 
@@ -285,6 +291,7 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits)
     }
 }
 
+// (8 / 16 / 32 / 64 KB: 65 / 52 / 56 / 56 us for 158 states of 1.1 MB)
 constexpr long long kChunk = 16384;  // bytes of a pool one workgroup copies
 
 // Workgroups (beam, chunk): the beam's place among its parent's children says whether it keeps

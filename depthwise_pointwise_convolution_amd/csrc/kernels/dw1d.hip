@@ -1,5 +1,9 @@
 // dw1d.hip -- causal depthwise layer along the token axis, for packed prompts and for one
 // token of each sequence:  y[t] = act(bias + sum_k w[k] * x[t - (W-1) + k])  per channel.
+//
+// W multiply-adds an element: HBM bounds it.  On MI355X, 8192 tokens x 4096 bf16 channels, W = 4:
+// 33 us, 4.1 TB/s of the 134 MB that have to move (a large copy reaches 5.2); one token of 96
+// sequences: 3.8 us on the device, most of it launch and one memory latency.
 #include "seq_common.h"
 #include "../seq.h"
 
@@ -76,8 +80,10 @@ __global__ __launch_bounds__(256) void dw1d_fwd_kernel(Dw1dArgs a, int cblocks, 
     T* y = (T*)a.y;
     T* state = (T*)a.state;
     const int runs = (a.tokens + kRun - 1) / kRun;
-    // An output larger than the L2s together (32 MB) leaves them during the kernel, not in the
-    // write-back at its end: 36 -> 31 us for 64 MB.  A smaller one stays for whoever reads it next.
+    // An output larger than the L2s together (32 MB) is stored past them.  Alone that gains (64 MB:
+    // 37.5 -> 33 us, 128 MB: 65 -> 59), and with the projection that reads it next too from 128 MB on
+    // (129 -> 123 us, 64 MB: 81 both ways); below 32 MB that reader finds it in the L2s (32 MB: 48
+    // against 49 us, 2 MB: 18 against 19).
     const bool past_l2 = (long long)a.tokens * a.D * (int)sizeof(T) > (32ll << 20);
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const int row = (int)(u / cblocks);
@@ -115,10 +121,13 @@ __global__ __launch_bounds__(256) void dw1d_fwd_kernel(Dw1dArgs a, int cblocks, 
                 for (int k = 0; k < W; ++k) win[i + k].get(in[k]);
                 taps.apply(in, a.silu, out);
                 T* to = y + t * a.ldy + c;
-                if (V == Vec<T>::N && past_l2)
+                if (V == Vec<T>::N && past_l2) {
+                    asm volatile("");  // (or both stores become one, which does not stream)
                     __builtin_nontemporal_store(pack16<T>(out), (u32x4*)to);
-                else
+                    asm volatile("");
+                } else {
                     store_row<T, V>(to, out);
+                }
             }
         } else {
             const int seq = row - runs;

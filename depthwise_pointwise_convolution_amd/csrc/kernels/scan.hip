@@ -1,6 +1,17 @@
 // scan.hip -- selective state-space scan, for packed prompts and for one token of each
 // sequence.  Per channel d and state n:
 //   h = exp(delta * A) * h + delta * B * x,   y = (sum_n C * h + skip * x) * silu(z).
+//
+// Prompts: an element of x takes N exponentials (two issue slots each) and 4 N multiplies and
+// multiply-adds, about 130 slots with N = 16 against 8 bytes: the vector units bound it.  The
+// recurrence leaves D * seqs independent chains, too few for 1024 SIMDs, so long sequences are cut
+// into chunks and scanned twice, 11/6 of the work.  On MI355X: eleven prompts, 8192 tokens x 4096
+// fp16 channels in all, N = 16: 239 us (first pass 100, join 17, second pass 130; a pass without
+// the cut would take 110 at the vector units' peak, the bytes 53); one prompt of 2048 x 2048 bf16:
+// 51 us.  In both passes the vector units are busy 84% of the time (counters).
+//
+// One token: the fp32 state is read and written, 8 N bytes a channel: HBM bounds it.  256 tokens x
+// 4096 channels: 26 us, 5.5 TB/s.
 #include <float.h>
 
 #include "seq_common.h"
