@@ -2,7 +2,7 @@
 // token of each sequence:  y[t] = act(bias + sum_k w[k] * x[t - (W-1) + k])  per channel.
 //
 // W multiply-adds an element: HBM bounds it.  On MI355X, 8192 tokens x 4096 bf16 channels, W = 4:
-// 33 us, 4.1 TB/s of the 134 MB that have to move (a large copy reaches 5.2); one token of 96
+// 30 us, 4.5 TB/s of the 134 MB that have to move (a large copy reaches 5.2); one token of 96
 // sequences: 3.8 us on the device, most of it launch and one memory latency.
 #include "seq_common.h"
 #include "../seq.h"
@@ -10,8 +10,8 @@
 namespace fcm {
 namespace {
 
-// Tokens of one workgroup: with 4 / 8 / 16 an 8192 x 4096 bf16 layer takes 36 / 31 / 31 us (fewer
-// re-read more rows at their start).
+// Tokens of one workgroup: with 4 / 8 / 12 / 16 an 8192 x 4096 bf16 layer takes 36 / 30 / 31 / 31 us
+// (fewer re-read more rows at their start; more than four waves a SIMD would spill them).
 constexpr int kRun = 8;
 
 template <typename T, int W, int V>
@@ -85,7 +85,9 @@ __global__ __launch_bounds__(256) void dw1d_fwd_kernel(Dw1dArgs a, int cblocks, 
     // (129 -> 123 us, 64 MB: 81 both ways); below 32 MB that reader finds it in the L2s (32 MB: 48
     // against 49 us, 2 MB: 18 against 19).
     const bool past_l2 = (long long)a.tokens * a.D * (int)sizeof(T) > (32ll << 20);
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    // Neighbouring runs, which read the same rows at their seam, on one XCD and its L2: 93 -> 68 MB
+    // of reads for the layer above, at the same time.
+    for (long long u = xcd_logical_id(blockIdx.x, gridDim.x); u < units; u += gridDim.x) {
         const int row = (int)(u / cblocks);
         const int c = (int)((u % cblocks) * blockDim.x + threadIdx.x) * V;
         const bool live = c < a.D;
@@ -214,7 +216,7 @@ int launch(const Dw1dArgs& a, bool step, void* stream) {
     const int cblocks = (vecs + block - 1) / block;
     const long long rows = step ? a.seqs : (a.tokens + kRun - 1) / kRun + (long long)a.seqs;
     const long long units = rows * cblocks;
-    const int grid = (int)(units < (1 << 22) ? units : (1 << 22));
+    const int grid = (int)(units < (1 << 22) ? (units + 7) / 8 * 8 : (1 << 22));
     if (step)
         dw1d_step_kernel<T, W, V><<<grid, block, 0, (hipStream_t)stream>>>(a, cblocks, units);
     else

@@ -299,10 +299,10 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a, int len, int
         }
         count = __shfl(count, seq & 63);
         if (before + count > chunks) count = chunks - before;
-        const long long i = (u % blocks) * 256 + threadIdx.x;
+        const uint32_t i = (uint32_t)(u % blocks) * 256 + threadIdx.x;  // (N * D is at most 2^30)
         if (count <= 2 || i >= plane) continue;
-        const int d = (int)(i % a.D);
-        const float A = rate2(a.A[(long long)d * a.N + i / a.D]);
+        const uint32_t d = i % (uint32_t)a.D;
+        const float A = rate2(a.A[(long long)d * a.N + i / (uint32_t)a.D]);
         float* s = starts + (long long)before * plane + i;
         const float* w = sums + (long long)before * a.D + d;
         float add[kJoin], sum[kJoin];
