@@ -199,6 +199,9 @@ __global__ __launch_bounds__(256, 8) void beam_rows_kernel(BeamArgs a, int split
         lane < have && key_token(mine) < a.vocab ? mine : 0;
 }
 
+// (Rows and merge in one launch, sixteen waves a request, saves a launch but reads a row's blocks
+// one after the other, 3 us each: 31 against 9.7 us for 4 rows of 32000.)
+//
 // One workgroup per request.  A wave per beam (in turn): the splits' sums give the row's
 // log-sum-exp, and lane s walks split s's best tokens while the best head of all lanes is taken
 // W times.  Then the first wave does the same over the beams, on scores in 64 bits.

@@ -119,11 +119,11 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 
 // The scan of one chunk, in one of two passes.  Q neighbouring lanes have one channel, NP of its
-// N states each, in registers.  A sequence longer than a chunk is scanned twice, so that its chunks run at the same
-// time: LAST = false finds what a chunk adds to a state (from zero; the first chunk from the
-// sequence's own) and the sum of its steps, whose exponential is the chunk's whole decay;
-// scan_join_kernel adds up where every chunk starts; LAST = true starts there and gives outputs
-// and the sequence's final state.  Workspace: starts [chunks][N][D], then sums [chunks][D].
+// N states each, in registers.  A sequence longer than a chunk is scanned twice, so that its chunks
+// run at the same time: LAST = false finds what a chunk adds to a state (from zero; the first chunk
+// from the sequence's own) and the sum of its steps, whose exponential is the chunk's whole decay;
+// scan_join_kernel adds up where every chunk starts; LAST = true starts there and gives outputs and
+// the sequence's final state.  Workspace: starts [chunks][N][D], then sums [chunks][D].
 //
 // B and C are the same for all channels of a group: the workgroup converts them to fp32 in LDS
 // once a tile, and its lanes read them by broadcast, four states an instruction.
