@@ -153,6 +153,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libfcm.so (built in-tree by ``build.py``); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -232,9 +234,12 @@ def _ptr(t) -> Optional[int]:
     """Device address of a tensor (or an int address); None stays NULL."""
     if t is None:
         return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:
+        return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):  # an address
+            return t
+        raise
 
 
 _current_stream = None

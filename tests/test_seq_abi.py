@@ -84,6 +84,35 @@ def test_workspace_of_a_bad_problem():
     _refused(lambda: F.fcm_beam_workspace(F.beam_problem("f16", 1, 40, 100)), 1, "32 beams")
 
 
+@pytest.mark.parametrize("t", ["x", b"x", 1.0, [0]])
+def test_only_tensors_and_addresses_are_pointers(t):
+    F = _F()
+    with pytest.raises(AttributeError):
+        F._ptr(t)
+    assert F._ptr(None) is None and F._ptr(4096) == 4096
+
+
+@pytest.mark.parametrize("T,B,D,N,G", [(1, 1, 64, 16, 1), (9, 3, 64, 16, 1), (100, 7, 300, 5, 3), (2048, 1, 2048, 16, 1),
+                                       (777, 4, 1026, 24, 2), (8192, 11, 4096, 16, 1), (16000, 1, 256, 64, 1),
+                                       (65536, 2, 128, 8, 1), (500, 500, 64, 16, 1)])
+def test_scan_workspace_holds_the_chunks_of_any_split(T, B, D, N, G):
+    # the workspace has tokens // len + seqs chunks of (N + 1) * D floats, len a power of two; however
+    # the tokens are divided among the sequences, their chunks (one at least each) fit
+    import random
+    F = _F()
+    size = F.fcm_scan_workspace(F.scan_problem("bf16", D, N, groups=G, tokens=T, seqs=B))
+    if size == 0:
+        return
+    chunks, rest = divmod(size, (N + 1) * D * 4)
+    lens = [1 << k for k in range(3, 20) if T // (1 << k) + B == chunks]
+    assert rest == 0 and lens, (size, chunks)
+    r = random.Random(T)
+    for _ in range(50):
+        cuts = sorted(r.choice((0, T, r.randrange(T + 1))) for _ in range(B - 1))
+        parts = [b - a for a, b in zip([0] + cuts, cuts + [T])]
+        assert sum(max(1, -(-n // lens[0])) for n in parts) <= chunks
+
+
 Q4 = ("x", "q", "scales", "zeros", "bias", "y")
 
 
