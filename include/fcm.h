@@ -471,7 +471,7 @@ typedef struct {
 } fcm_scan_problem;
 
 /* Bytes of device memory fcm_scan_fwd needs for `prob` (0 if it needs none), or -1 if the
- * problem is invalid.  Host only. */
+ * problem is invalid or unsupported (fcm_last_error says why).  Host only. */
 int64_t fcm_scan_workspace(const fcm_scan_problem* prob);
 
 /* Prompts.  x, dt, z: [tokens][D] (z may be NULL); A: [D][N] fp32; Bm, Cm:
@@ -521,7 +521,7 @@ typedef struct {
     int64_t ldl;      /* row stride of the logits */
 } fcm_beam_problem;
 
-/* Bytes of device memory fcm_beam_select needs, or -1 if the problem is invalid. */
+/* Bytes of device memory fcm_beam_select needs, or -1 as for fcm_scan_workspace. */
 int64_t fcm_beam_workspace(const fcm_beam_problem* prob);
 
 /* The `beams` best continuations of each request among beams * vocab, best first:
