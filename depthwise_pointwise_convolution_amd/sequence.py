@@ -8,6 +8,10 @@ gated by the in-projection's other half -> out-projection:
     block = StateSpaceBlock(..., slots=16)
     y = block.prompt(x, cu, slots)        # packed prompts [tokens, dim]
     y = block.step(x, slots)              # one token of each sequence [batch, dim]
+
+Every call works on torch's current stream.  With ``stream`` (a torch stream or a raw handle) all of
+it, the projections and what it allocates among it, works on that stream instead, behind what the
+current stream holds at the call; whoever uses the results or the states on another stream waits for it.
 """
 from __future__ import annotations
 
@@ -37,6 +41,27 @@ def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, name: str):
 def _stride(t: torch.Tensor) -> int:
     """Row stride; a single row has none that matters."""
     return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _on(stream, call, *tensors):
+    """`call` with all its work on `stream`.  The allocator hands memory out by stream: what `call`
+    makes belongs to `stream`, the caller's `tensors` may be freed while it still uses them, and so may the
+    results while the current stream does; each is told of the other."""
+    if not hasattr(stream, "wait_stream"):  # a raw handle, 0 the default stream's
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    here = torch.cuda.current_stream()
+    if stream == here:
+        return call()
+    stream.wait_stream(here)
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        result = call()
+    for t in result if isinstance(result, tuple) else (result,):
+        if t.is_cuda:
+            t.record_stream(here)
+    return result
 
 
 def quantize_q4(weight: torch.Tensor, group: int = 128, symmetric: bool = False):
@@ -98,6 +123,8 @@ class Q4Linear:
         return (q - zero) * self.scales.float()[:, at]
 
     def __call__(self, x, out=None, stream=None) -> torch.Tensor:
+        if stream is not None:
+            return _on(stream, lambda: self(x, out), x, out)
         x = _rows(x, self.C, self.dtype, "x")
         if x.data_ptr() % 16 or _stride(x) % 8:
             x = x.contiguous()
@@ -107,7 +134,7 @@ class Q4Linear:
         _rows(out, self.K, self.dtype, "out")
         fcm_q4_fwd(q4_problem(DTYPE_NAMES[self.dtype], M, self.C, self.K, group=self.group,
                               act=self.act, ldx=_stride(x), ldy=_stride(out)),
-                   x, self.q, self.scales, self.zeros, self.bias, out, stream)
+                   x, self.q, self.scales, self.zeros, self.bias, out)
         return out
 
 
@@ -154,6 +181,8 @@ class StateSpaceBlock:
     def prompt(self, x, cu, slots, carry=None, stream=None) -> torch.Tensor:
         """x: [tokens, dim], sequence b in rows cu[b] .. cu[b+1]-1 and state slot slots[b]; with
         carry[b] != 0 it continues from there."""
+        if stream is not None:
+            return _on(stream, lambda: self.prompt(x, cu, slots, carry), x, cu, slots, carry)
         T, B = x.shape[0], slots.shape[0]
         self._index(cu, B + 1, "cu")
         self._index(slots, B, "slots")
@@ -163,18 +192,20 @@ class StateSpaceBlock:
         u = torch.empty(T, self.inner, dtype=self.dtype, device=x.device)
         fcm_dw1d_fwd(dw1d_problem(self.name, self.inner, self.W, tokens=T, seqs=B,
                                   slots=self.slots, ldx=_stride(xs)),
-                     xs, self.conv_w, self.conv_b, cu, slots, carry, self.window, u, stream)
+                     xs, self.conv_w, self.conv_b, cu, slots, carry, self.window, u)
         dt, b, c = self._parts(u)
         y = torch.empty_like(u)
         prob = scan_problem(self.name, self.inner, self.N, tokens=T, seqs=B, slots=self.slots,
                             lddt=_stride(dt), ldb=_stride(b), ldc=_stride(c), ldz=_stride(z))
         ws = torch.empty(max(16, fcm_scan_workspace(prob)), dtype=torch.uint8, device=x.device)
         fcm_scan_fwd(prob, u, dt, self.A, b, c, self.skip, self.dt_bias, z, cu, slots, carry,
-                     self.state, ws, y, stream)
+                     self.state, ws, y)
         return self.out_proj(y)
 
     def step(self, x, slots, stream=None) -> torch.Tensor:
         """x: [batch, dim], one token of the sequence in slots[b] (outside [0, slots): an idle row)."""
+        if stream is not None:
+            return _on(stream, lambda: self.step(x, slots), x, slots)
         B = x.shape[0]
         self._index(slots, B, "slots")
         xz = self.in_proj(x)
@@ -182,13 +213,13 @@ class StateSpaceBlock:
         u = torch.empty(B, self.inner, dtype=self.dtype, device=x.device)
         fcm_dw1d_step(dw1d_problem(self.name, self.inner, self.W, tokens=B, seqs=B,
                                    slots=self.slots, ldx=_stride(xs)),
-                      xs, self.conv_w, self.conv_b, slots, self.window, u, stream)
+                      xs, self.conv_w, self.conv_b, slots, self.window, u)
         dt, b, c = self._parts(u)
         y = torch.empty_like(u)
         fcm_scan_step(scan_problem(self.name, self.inner, self.N, tokens=B, seqs=B,
                                    slots=self.slots, lddt=_stride(dt), ldb=_stride(b),
                                    ldc=_stride(c), ldz=_stride(z)),
-                      u, dt, self.A, b, c, self.skip, self.dt_bias, z, slots, self.state, y, stream)
+                      u, dt, self.A, b, c, self.skip, self.dt_bias, z, slots, self.state, y)
         return self.out_proj(y)
 
 
@@ -218,6 +249,8 @@ class BeamSearch:
         """Takes the logits [requests*beams, vocab] of the beams' last tokens, picks the next beams,
         and moves the states in `pools` ([slots, ...], contiguous) to them.  Returns (parent, token);
         scores, done and slots are the new beams'."""
+        if stream is not None:
+            return _on(stream, lambda: self.advance(logits, pools), logits, *pools)
         n = self.requests * self.beams
         _need(logits.dtype in DTYPE_NAMES, "logits must be float32, float16 or bfloat16")
         logits = _rows(logits, self.vocab, logits.dtype, "logits")
@@ -231,9 +264,9 @@ class BeamSearch:
                                    device=logits.device)
         scores, done, slots = self._next
         fcm_beam_select(prob, logits, self.scores, self.done if self.eos >= 0 else None, self._ws,
-                        scores, self.parent, self.token, done, stream)
+                        scores, self.parent, self.token, done)
         for i in range(0, len(pools), 8) or (0,):
-            fcm_beam_reorder(prob, self.parent, self.slots, slots, list(pools[i:i + 8]), stream)
+            fcm_beam_reorder(prob, self.parent, self.slots, slots, list(pools[i:i + 8]))
         self._next = (self.scores, self.done, self.slots)
         self.scores, self.done, self.slots = scores, done, slots
         return self.parent, self.token

@@ -1,0 +1,122 @@
+"""The sequence operators' wrappers with their launches stubbed (no GPU): what they pass on, on which
+stream, and what they refuse."""
+import contextlib
+
+import pytest
+import torch
+
+import depthwise_pointwise_convolution_amd.sequence as S
+
+z = torch.zeros
+BF = torch.bfloat16
+
+
+class Calls(list):
+    """(name, problem, pointer arguments, stream) of the launches."""
+
+    def names(self):
+        return [c[0] for c in self]
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    got = Calls()
+
+    def stub(name):
+        def launch(prob, *args, stream=None):
+            n = {"fcm_dw1d_fwd": 8, "fcm_dw1d_step": 6, "fcm_scan_fwd": 14, "fcm_scan_step": 11, "fcm_q4_fwd": 6,
+                 "fcm_beam_select": 8, "fcm_beam_reorder": 4}[name]
+            if len(args) > n:
+                args, stream = args[:n], args[n]
+            # the stream it runs on: the one passed, or what is current by then
+            got.append((name, prob, args, torch.cuda.current_stream() if stream is None else stream))
+        return launch
+
+    for name in ("fcm_dw1d_fwd", "fcm_dw1d_step", "fcm_scan_fwd", "fcm_scan_step", "fcm_q4_fwd", "fcm_beam_select",
+                 "fcm_beam_reorder"):
+        monkeypatch.setattr(S, name, stub(name))
+    monkeypatch.setattr(S, "fcm_scan_workspace", lambda prob: 64)
+    monkeypatch.setattr(S, "fcm_beam_workspace", lambda prob: 64)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: None)
+    # CPU tensors stand for those of the GPU
+    monkeypatch.setattr(S, "_on_gpu", lambda t: True, raising=False)
+    return got
+
+
+def linear(C, K, dtype=BF):
+    return S.Q4Linear(z(K, C // 2, dtype=torch.uint8), z(K, -(-C // 32), dtype=dtype), group=32)
+
+
+def block(inner=16, N=4, rank=8, dim=24, dtype=BF, **k):
+    parts = {"in_proj": linear(dim, 2 * inner, dtype), "x_proj": linear(inner, rank + 2 * N, dtype),
+             "dt_proj": linear(rank, inner, dtype), "out_proj": linear(inner, dim, dtype), **k}
+    return S.StateSpaceBlock(parts["in_proj"], z(inner, 4, dtype=dtype), None, parts["x_proj"], parts["dt_proj"], None,
+                             z(inner, N), None, parts["out_proj"], slots=3)
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+# ------------------------------------------------------------------------------------------
+# streams
+# ------------------------------------------------------------------------------------------
+class Stream:
+    def __init__(self, name):
+        self.name, self.waited = name, []
+
+    def wait_stream(self, other):
+        self.waited.append(other)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """(the caller's stream, another one, what is the current one)."""
+    now = [Stream("caller")]
+
+    @contextlib.contextmanager
+    def use(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    return now[0], Stream("other"), now
+
+
+@pytest.mark.parametrize("what", ["prompt", "step", "linear", "advance"])
+def test_a_stream_takes_the_whole_call(calls, streams, monkeypatch, what):
+    # projections, allocations and launches: all on the stream that was given, behind the caller's
+    caller, other, now = streams
+    seen = []
+
+    def watched(f):
+        def call(x):
+            seen.append(now[-1])
+            return f(x)
+        return call
+
+    for name in ("empty", "empty_like"):
+        def made(*a, real=getattr(torch, name), **k):
+            seen.append(now[-1])
+            return real(*a, **k)
+        monkeypatch.setattr(torch, name, made)
+    b = block(in_proj=watched(linear(24, 32)), x_proj=watched(linear(16, 16)), dt_proj=watched(linear(8, 16)),
+              out_proj=watched(linear(16, 24)))
+    search = S.BeamSearch(1, 2, 10, ints(0, 1))
+    lin = linear(64, 8)
+    seen.clear()
+    if what == "prompt":
+        b.prompt(z(5, 24, dtype=BF), ints(0, 2, 5), ints(0, 1), stream=other)
+    elif what == "step":
+        b.step(z(2, 24, dtype=BF), ints(0, 1), stream=other)
+    elif what == "linear":
+        # (an input that has to be laid out first)
+        lin(z(4, 66, dtype=BF)[:, 1:65], stream=other)
+    else:
+        search.advance(z(2, 10), [z(2, 8)], stream=other)
+    assert calls
+    seen += [c[3] for c in calls]
+    assert all(s is other for s in seen), [s.name for s in seen]
+    assert other.waited == [caller] and now == [caller]
