@@ -35,7 +35,9 @@ def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, name: str):
     _need(t.dim() == 2 and t.shape[1] == width, f"{name} must be [rows, {width}]")
     _need(t.dtype == dtype, f"{name} must be {dtype}")
     _need(t.shape[0] <= 1 or t.stride(1) == 1, f"{name}'s channels must be contiguous")
-    return t if width == 1 or t.stride(1) == 1 else t.contiguous()
+    # (rows that overlap, as a broadcast one does, have no row stride that the library takes)
+    apart = t.shape[0] <= 1 or t.stride(0) >= width
+    return t if apart and (width == 1 or t.stride(1) == 1) else t.contiguous()
 
 
 def _stride(t: torch.Tensor) -> int:

@@ -120,3 +120,44 @@ def test_a_stream_takes_the_whole_call(calls, streams, monkeypatch, what):
     seen += [c[3] for c in calls]
     assert all(s is other for s in seen), [s.name for s in seen]
     assert other.waited == [caller] and now == [caller]
+
+
+# ------------------------------------------------------------------------------------------
+# broadcast inputs
+# ------------------------------------------------------------------------------------------
+def _strided_rows(prob, ld, t, rows, width):
+    """Whether the launch reads `rows` rows of `t` inside its storage."""
+    pitch = getattr(prob, ld) or width
+    last = t.storage_offset() + (rows - 1) * pitch + width
+    return last * t.element_size() <= t.untyped_storage().nbytes()
+
+
+def test_broadcast_rows_are_laid_out(calls):
+    # a stride of 0 means densely packed rows in the library: one row that stands for several, and
+    # rows that overlap, are copied before
+    row = torch.arange(64, dtype=BF)[None]
+    lin = linear(64, 8)
+    for x in (row.expand(4, 64), torch.arange(100, dtype=BF).as_strided((4, 64), (8, 1))):
+        calls.clear()
+        lin(x)
+        (_, prob, args, _), = calls
+        assert prob.M == 4 and _strided_rows(prob, "ldx", args[0], 4, 64)
+        assert torch.equal(args[0], x)
+    # a first step's logits: the same row for every beam
+    search = S.BeamSearch(2, 3, 10, ints(*range(6)))
+    logits = torch.randn(1, 10).expand(6, 10)
+    calls.clear()
+    search.advance(logits, [])
+    prob, args = calls[0][1:3]
+    assert _strided_rows(prob, "ldl", args[0], 6, 10) and torch.equal(args[0], logits)
+    # one column: its rows may stand anywhere
+    search = S.BeamSearch(1, 4, 1, ints(*range(4)))
+    calls.clear()
+    search.advance(z(1, 1).expand(4, 1), [])
+    assert _strided_rows(calls[0][1], "ldl", calls[0][2][0], 4, 1)
+
+
+def test_strided_rows_are_taken_as_they_are(calls):
+    wide = z(4, 96, dtype=BF)
+    linear(64, 8)(wide[:, :64])
+    assert calls[0][1].ldx == 96 and calls[0][2][0].data_ptr() == wide.data_ptr()

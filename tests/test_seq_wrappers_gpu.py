@@ -57,3 +57,17 @@ def test_wrappers_on_a_stream_give_what_they_give_without(how):
         got.append([t.clone() for t in out])
     for i, (a, b) in enumerate(zip(*got)):
         assert torch.equal(a, b), i
+
+
+def test_broadcast_rows_give_what_their_copies_give():
+    import depthwise_pointwise_convolution_amd.sequence as S
+    g = torch.Generator().manual_seed(3)
+    lin = _linear(S, g, 128, 500)
+    row = torch.randn(1, 128, generator=g).to(BF).cuda()
+    y = lin(row.expand(7, 128))
+    assert torch.equal(y, lin(row.repeat(7, 1)))
+    slots = torch.arange(4, dtype=torch.int32).cuda()
+    one, all_ = S.BeamSearch(1, 4, 500, slots), S.BeamSearch(1, 4, 500, slots)
+    pools = [torch.randn(4, 8, generator=g).cuda()]
+    a, b = one.advance(y[:1].expand(4, 500), pools), all_.advance(y[:4], [pools[0].clone()])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(one.scores, all_.scores)
