@@ -40,6 +40,15 @@ def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, name: str):
     return t if apart and (width == 1 or t.stride(1) == 1) else t.contiguous()
 
 
+def _out(t: torch.Tensor, rows: int, width: int, dtype: torch.dtype):
+    """An output is written where it lies (its first `rows` rows), so its rows have to be apart and their
+    channels dense."""
+    _need(t.dim() == 2 and t.shape[0] >= rows and t.shape[1] == width and t.dtype == dtype,
+          f"out must be [{rows}, {width}] {dtype}")
+    _need(width == 1 or t.stride(1) == 1, "out's channels must be contiguous")
+    _need(t.shape[0] <= 1 or t.stride(0) >= width, "out's rows must not overlap")
+
+
 def _stride(t: torch.Tensor) -> int:
     """Row stride; a single row has none that matters."""
     return t.stride(0) if t.shape[0] > 1 else 0
@@ -133,7 +142,8 @@ class Q4Linear:
         M = x.shape[0]
         if out is None:
             out = torch.empty(M, self.K, dtype=self.dtype, device=x.device)
-        _rows(out, self.K, self.dtype, "out")
+        else:
+            _out(out, M, self.K, self.dtype)
         fcm_q4_fwd(q4_problem(DTYPE_NAMES[self.dtype], M, self.C, self.K, group=self.group,
                               act=self.act, ldx=_stride(x), ldy=_stride(out)),
                    x, self.q, self.scales, self.zeros, self.bias, out)

@@ -161,3 +161,30 @@ def test_strided_rows_are_taken_as_they_are(calls):
     wide = z(4, 96, dtype=BF)
     linear(64, 8)(wide[:, :64])
     assert calls[0][1].ldx == 96 and calls[0][2][0].data_ptr() == wide.data_ptr()
+
+
+# ------------------------------------------------------------------------------------------
+# outputs
+# ------------------------------------------------------------------------------------------
+def test_an_output_that_the_kernel_would_miss_is_refused(calls):
+    lin, x = linear(64, 8), z(4, 64, dtype=BF)
+    for x_, out in ((x, z(2, 8, dtype=BF)), (x, z(4, 9, dtype=BF)), (x, z(4, 8)),
+                    (x, z(8, 4, dtype=BF).t()), (x, z(1, 8, dtype=BF).expand(4, 8)),
+                    (x, z(60, dtype=BF).as_strided((4, 8), (4, 1))),
+                    (x[:1], z(8, 2, dtype=BF)[:, 1:2].t())):
+        with pytest.raises(ValueError, match="out"):
+            lin(x_, out=out)
+    assert not calls
+
+
+def test_outputs_that_fit_are_written_in_place(calls):
+    lin, x = linear(64, 8), z(4, 64, dtype=BF)
+    wide = z(4, 24, dtype=BF)
+    for x_, out in ((x, wide[:, 8:16]), (x, z(4, 8, dtype=BF)), (x, z(6, 8, dtype=BF)), (x[:1], z(1, 8, dtype=BF)), (x[:1], wide[2:3, 3:11]),
+                    (x[:0], z(0, 8, dtype=BF))):
+        calls.clear()
+        assert lin(x_, out=out) is out
+        assert calls[0][2][5].data_ptr() == out.data_ptr()
+    one = linear(64, 1)
+    out = z(1, 7, dtype=BF)[:, 2:3]
+    assert one(x[:1], out=out) is out
