@@ -179,12 +179,26 @@ class StateSpaceBlock:
         self.state = torch.zeros(slots, self.inner, self.N, device=conv_w.device)
         self.name = DTYPE_NAMES[self.dtype]
 
+    def _projected(self, p, rows: int, width: int, name: str):
+        """What a projection gave, in the form the kernels take its rows."""
+        name = f"{name}'s result"
+        p = _rows(p, width, self.dtype, name)
+        _need(p.shape[0] == rows, f"{name} must have {rows} rows")
+        return p
+
+    def _halves(self, x):
+        """(scan input, gate): the in-projection's two halves."""
+        xz = self._projected(self.in_proj(x), x.shape[0], 2 * self.inner, "in_proj")
+        return xz[:, :self.inner], xz[:, self.inner:]
+
     def _parts(self, u):
         """(step, B, C) of the depthwise layer's output."""
         p = self.x_proj(u)
+        _need(p.dim() == 2 and p.shape[1] > 2 * self.N, "x_proj must give the step's rows and then B and C")
         rank = p.shape[1] - 2 * self.N
-        _need(rank > 0, "x_proj must give the step's rows and then B and C")
-        return self.dt_proj(p[:, :rank]), p[:, rank:rank + self.N], p[:, rank + self.N:]
+        p = self._projected(p, u.shape[0], p.shape[1], "x_proj")
+        dt = self._projected(self.dt_proj(p[:, :rank]), u.shape[0], self.inner, "dt_proj")
+        return dt, p[:, rank:rank + self.N], p[:, rank + self.N:]
 
     def _index(self, t, n: int, name: str):
         _need(t is None or (t.dtype == torch.int32 and tuple(t.shape) == (n,) and t.is_contiguous()),
@@ -199,8 +213,7 @@ class StateSpaceBlock:
         self._index(cu, B + 1, "cu")
         self._index(slots, B, "slots")
         self._index(carry, B, "carry")
-        xz = self.in_proj(x)
-        xs, z = xz[:, :self.inner], xz[:, self.inner:]
+        xs, z = self._halves(x)
         u = torch.empty(T, self.inner, dtype=self.dtype, device=x.device)
         fcm_dw1d_fwd(dw1d_problem(self.name, self.inner, self.W, tokens=T, seqs=B,
                                   slots=self.slots, ldx=_stride(xs)),
@@ -220,8 +233,7 @@ class StateSpaceBlock:
             return _on(stream, lambda: self.step(x, slots), x, slots)
         B = x.shape[0]
         self._index(slots, B, "slots")
-        xz = self.in_proj(x)
-        xs, z = xz[:, :self.inner], xz[:, self.inner:]
+        xs, z = self._halves(x)
         u = torch.empty(B, self.inner, dtype=self.dtype, device=x.device)
         fcm_dw1d_step(dw1d_problem(self.name, self.inner, self.W, tokens=B, seqs=B,
                                    slots=self.slots, ldx=_stride(xs)),

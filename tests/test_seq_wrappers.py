@@ -188,3 +188,39 @@ def test_outputs_that_fit_are_written_in_place(calls):
     one = linear(64, 1)
     out = z(1, 7, dtype=BF)[:, 2:3]
     assert one(x[:1], out=out) is out
+
+
+# ------------------------------------------------------------------------------------------
+# what a block's projections give
+# ------------------------------------------------------------------------------------------
+def _gives(t):
+    return lambda x: t
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("in_proj", z(2, 16, dtype=BF)), ("in_proj", z(2, 33, dtype=BF)), ("in_proj", z(1, 32, dtype=BF)),
+    ("in_proj", z(2, 32)), ("in_proj", z(32, 2, dtype=BF).t()), ("in_proj", z(2, 64, dtype=BF)[:, ::2]),
+    ("in_proj", z(64, dtype=BF)), ("x_proj", z(1, 16, dtype=BF)), ("x_proj", z(2, 16)), ("x_proj", z(2, 8, dtype=BF)),
+    ("x_proj", z(2, 32, dtype=BF)[:, ::2]), ("x_proj", z(32, dtype=BF)), ("dt_proj", z(2, 15, dtype=BF)),
+    ("dt_proj", z(1, 16, dtype=BF)), ("dt_proj", z(2, 16)), ("dt_proj", z(16, 2, dtype=BF).t())])
+def test_projections_of_another_form_are_refused(calls, name, bad):
+    # (their memory is handed to the kernels, which would read past it or other values than meant)
+    b = block(**{name: _gives(bad)})
+    with pytest.raises(ValueError, match=name):
+        b.prompt(z(2, 24, dtype=BF), ints(0, 2), ints(0))
+    with pytest.raises(ValueError, match=name):
+        b.step(z(2, 24, dtype=BF), ints(0, 1))
+
+
+def test_projections_that_broadcast_a_row_are_laid_out(calls):
+    rows = {"in_proj": z(1, 32, dtype=BF).expand(3, 32), "x_proj": z(1, 16, dtype=BF).expand(3, 16),
+            "dt_proj": z(1, 16, dtype=BF).expand(3, 16)}
+    b = block(**{k: _gives(v) for k, v in rows.items()})
+    b.step(z(3, 24, dtype=BF), ints(0, 1, 2))
+    b.prompt(z(3, 24, dtype=BF), ints(0, 2, 3), ints(0, 1))
+    for name, prob, args, _ in calls:
+        if name.startswith("fcm_dw1d"):
+            assert _strided_rows(prob, "ldx", args[0], 3, 16)
+        if name.startswith("fcm_scan"):
+            for ld, at, width in (("ldx", 0, 16), ("lddt", 1, 16), ("ldb", 3, 4), ("ldc", 4, 4), ("ldz", 7, 16)):
+                assert _strided_rows(prob, ld, args[at], 3, width), ld
