@@ -31,7 +31,18 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, name: str):
+def _on_gpu(t: torch.Tensor) -> bool:
+    """On the GPU whose stream the launches go to."""
+    return t.is_cuda and t.get_device() == torch.cuda.current_device()
+
+
+def _beside(t: torch.Tensor, device: torch.device, name: str):
+    """(a kernel that is given an address of another device, or of the host, faults)"""
+    _need(t.device == device, f"{name} must be on {device}")
+
+
+def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, name: str, device: torch.device):
+    _beside(t, device, name)
     _need(t.dim() == 2 and t.shape[1] == width, f"{name} must be [rows, {width}]")
     _need(t.dtype == dtype, f"{name} must be {dtype}")
     _need(t.shape[0] <= 1 or t.stride(1) == 1, f"{name}'s channels must be contiguous")
@@ -40,9 +51,10 @@ def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, name: str):
     return t if apart and (width == 1 or t.stride(1) == 1) else t.contiguous()
 
 
-def _out(t: torch.Tensor, rows: int, width: int, dtype: torch.dtype):
+def _out(t: torch.Tensor, rows: int, width: int, dtype: torch.dtype, device: torch.device):
     """An output is written where it lies (its first `rows` rows), so its rows have to be apart and their
     channels dense."""
+    _beside(t, device, "out")
     _need(t.dim() == 2 and t.shape[0] >= rows and t.shape[1] == width and t.dtype == dtype,
           f"out must be [{rows}, {width}] {dtype}")
     _need(width == 1 or t.stride(1) == 1, "out's channels must be contiguous")
@@ -117,6 +129,9 @@ class Q4Linear:
               f"zeros must be [{self.K}, {groups}] uint8")
         _need(bias is None or (bias.dtype == torch.float32 and tuple(bias.shape) == (self.K,) and
                                bias.is_contiguous()), f"bias must be [{self.K}] float32")
+        for name, v in (("scales", scales), ("zeros", zeros), ("bias", bias)):
+            if v is not None:
+                _beside(v, q.device, name)
         _need(act in ACT_CODES, f"act must be one of {sorted(ACT_CODES)}")
         self.q, self.scales, self.zeros, self.bias = q, scales, zeros, bias
         self.group, self.act, self.dtype = group, act, scales.dtype
@@ -136,14 +151,15 @@ class Q4Linear:
     def __call__(self, x, out=None, stream=None) -> torch.Tensor:
         if stream is not None:
             return _on(stream, lambda: self(x, out), x, out)
-        x = _rows(x, self.C, self.dtype, "x")
+        _need(_on_gpu(self.q), "the weights must be on the current GPU")
+        x = _rows(x, self.C, self.dtype, "x", self.q.device)
         if x.data_ptr() % 16 or _stride(x) % 8:
             x = x.contiguous()
         M = x.shape[0]
         if out is None:
             out = torch.empty(M, self.K, dtype=self.dtype, device=x.device)
         else:
-            _out(out, M, self.K, self.dtype)
+            _out(out, M, self.K, self.dtype, x.device)
         fcm_q4_fwd(q4_problem(DTYPE_NAMES[self.dtype], M, self.C, self.K, group=self.group,
                               act=self.act, ldx=_stride(x), ldy=_stride(out)),
                    x, self.q, self.scales, self.zeros, self.bias, out)
@@ -170,6 +186,9 @@ class StateSpaceBlock:
         for name, v in (("conv_b", conv_b), ("dt_bias", dt_bias), ("skip", skip)):
             _need(v is None or (tuple(v.shape) == (self.inner,) and v.dtype == torch.float32 and
                                 v.is_contiguous()), f"{name} must be [{self.inner}] float32")
+        for name, v in (("A", A), ("conv_b", conv_b), ("dt_bias", dt_bias), ("skip", skip)):
+            if v is not None:
+                _beside(v, conv_w.device, name)
         self.in_proj, self.x_proj, self.dt_proj, self.out_proj = in_proj, x_proj, dt_proj, out_proj
         self.conv_w, self.conv_b, self.dt_bias, self.A, self.skip = (
             conv_w.contiguous(), conv_b, dt_bias, A, skip)
@@ -182,7 +201,7 @@ class StateSpaceBlock:
     def _projected(self, p, rows: int, width: int, name: str):
         """What a projection gave, in the form the kernels take its rows."""
         name = f"{name}'s result"
-        p = _rows(p, width, self.dtype, name)
+        p = _rows(p, width, self.dtype, name, self.window.device)
         _need(p.shape[0] == rows, f"{name} must have {rows} rows")
         return p
 
@@ -201,6 +220,8 @@ class StateSpaceBlock:
         return dt, p[:, rank:rank + self.N], p[:, rank + self.N:]
 
     def _index(self, t, n: int, name: str):
+        if t is not None:
+            _beside(t, self.window.device, name)
         _need(t is None or (t.dtype == torch.int32 and tuple(t.shape) == (n,) and t.is_contiguous()),
               f"{name} must be [{n}] int32")
 
@@ -209,6 +230,7 @@ class StateSpaceBlock:
         carry[b] != 0 it continues from there."""
         if stream is not None:
             return _on(stream, lambda: self.prompt(x, cu, slots, carry), x, cu, slots, carry)
+        _need(_on_gpu(self.window), "the block must be on the current GPU")
         T, B = x.shape[0], slots.shape[0]
         self._index(cu, B + 1, "cu")
         self._index(slots, B, "slots")
@@ -231,6 +253,7 @@ class StateSpaceBlock:
         """x: [batch, dim], one token of the sequence in slots[b] (outside [0, slots): an idle row)."""
         if stream is not None:
             return _on(stream, lambda: self.step(x, slots), x, slots)
+        _need(_on_gpu(self.window), "the block must be on the current GPU")
         B = x.shape[0]
         self._index(slots, B, "slots")
         xs, z = self._halves(x)
@@ -277,9 +300,11 @@ class BeamSearch:
             return _on(stream, lambda: self.advance(logits, pools), logits, *pools)
         n = self.requests * self.beams
         _need(logits.dtype in DTYPE_NAMES, "logits must be float32, float16 or bfloat16")
-        logits = _rows(logits, self.vocab, logits.dtype, "logits")
+        _need(_on_gpu(self.slots), "the search must be on the current GPU")
+        logits = _rows(logits, self.vocab, logits.dtype, "logits", self.slots.device)
         _need(logits.shape[0] == n, f"logits must have {n} rows")
         for p in pools:
+            _beside(p, logits.device, "a state pool")
             _need(p.is_contiguous(), "state pools must be contiguous")
         prob = beam_problem(DTYPE_NAMES[logits.dtype], self.requests, self.beams, self.vocab,
                             eos=self.eos, ldl=_stride(logits))

@@ -224,3 +224,43 @@ def test_projections_that_broadcast_a_row_are_laid_out(calls):
         if name.startswith("fcm_scan"):
             for ld, at, width in (("ldx", 0, 16), ("lddt", 1, 16), ("ldb", 3, 4), ("ldc", 4, 4), ("ldz", 7, 16)):
                 assert _strided_rows(prob, ld, args[at], 3, width), ld
+
+
+# ------------------------------------------------------------------------------------------
+# where tensors are
+# ------------------------------------------------------------------------------------------
+def test_tensors_that_are_not_on_the_gpu_are_refused(calls, monkeypatch):
+    # a kernel that follows a host address faults
+    lin, b, search = linear(64, 8), block(), S.BeamSearch(1, 2, 10, ints(0, 1))
+    monkeypatch.undo()
+    for call in (lambda: lin(z(2, 64, dtype=BF)), lambda: b.prompt(z(2, 24, dtype=BF), ints(0, 2), ints(0)),
+                 lambda: b.step(z(2, 24, dtype=BF), ints(0, 1)), lambda: search.advance(z(2, 10), [])):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+def test_tensors_on_different_devices_are_refused(calls):
+    # ("meta" stands for another device than the one of the weights)
+    def away(*s, dtype=BF):
+        return torch.empty(*s, dtype=dtype, device="meta")
+
+    i32 = {"dtype": torch.int32}
+    lin, b, search = linear(64, 8), block(), S.BeamSearch(1, 2, 10, ints(0, 1))
+    x, p = z(2, 64, dtype=BF), z(2, 24, dtype=BF)
+    q, s = z(8, 32, dtype=torch.uint8), z(8, 2, dtype=BF)
+    for call in (lambda: lin(away(2, 64)), lambda: lin(x, out=away(2, 8)),
+                 lambda: S.Q4Linear(q, away(8, 2), group=32),
+                 lambda: S.Q4Linear(q, s, zeros=away(8, 2, dtype=torch.uint8), group=32),
+                 lambda: S.Q4Linear(q, s, bias=away(8, dtype=torch.float32), group=32),
+                 lambda: b.prompt(p, away(2, **i32), ints(0)), lambda: b.prompt(p, ints(0, 2), away(1, **i32)),
+                 lambda: b.prompt(p, ints(0, 2), ints(0), carry=away(1, **i32)), lambda: b.step(p, away(2, **i32)),
+                 lambda: block(in_proj=_gives(away(2, 32))).step(p, ints(0, 1)),
+                 lambda: block(x_proj=_gives(away(2, 16))).step(p, ints(0, 1)),
+                 lambda: block(dt_proj=_gives(away(2, 16))).step(p, ints(0, 1)),
+                 lambda: S.StateSpaceBlock(None, z(8, 4), None, None, None, None, away(8, 4, dtype=torch.float32), None,
+                                           None, 1),
+                 lambda: S.StateSpaceBlock(None, z(8, 4), away(8, dtype=torch.float32), None, None, None, z(8, 4), None,
+                                           None, 1),
+                 lambda: search.advance(away(2, 10), []), lambda: search.advance(z(2, 10), [away(2, 8)])):
+        with pytest.raises(ValueError, match="must be on"):
+            call()
