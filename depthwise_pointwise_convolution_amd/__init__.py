@@ -560,13 +560,29 @@ def fcm_beam_select(prob, logits, scores, done, workspace, next_scores, parent, 
                                  _stream(stream)), "fcm_beam_select")
 
 
+def _slot_elements(t) -> int:
+    """Elements from one slot of a state array to the next.  A slot is copied as one run of them, so it
+    has to fill them, in whatever order of its axes."""
+    dense = getattr(t, "is_contiguous", None)
+    if dense is None or (t.shape[0] > 1 and dense()):
+        return t.stride(0)
+    size = 1
+    for step, n in sorted(zip(t.stride()[1:], t.shape[1:])):
+        if n != 1 and step != size:
+            raise ValueError("a state array's slots must be without gaps")
+        size *= n
+    if t.shape[0] > 1 and t.stride(0) != size:
+        raise ValueError("a state array's slots must lie one behind the other")
+    return size
+
+
 def fcm_beam_reorder(prob, parent, slots, next_slots, pools, stream=None):
-    """pools: state tensors whose first axis counts slots (contiguous)."""
+    """pools: state tensors whose first axis counts slots, which lie one behind the other without gaps."""
     n = len(pools)
     ptrs, bytes_, slots_ = _POINTERS(), _SIZES(), _SIZES()
     for i, t in zip(range(FCM_BEAM_POOLS), pools):  # (more are refused below)
         ptrs[i] = t.data_ptr()
-        bytes_[i] = t.stride(0) * t.element_size()
+        bytes_[i] = _slot_elements(t) * t.element_size()
         slots_[i] = t.shape[0]
     _check(lib().fcm_beam_reorder(prob, _ptr(parent), _ptr(slots), _ptr(next_slots), n, ptrs,
                                   bytes_, slots_, _stream(stream)), "fcm_beam_reorder")

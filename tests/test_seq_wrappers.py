@@ -264,3 +264,44 @@ def test_tensors_on_different_devices_are_refused(calls):
                  lambda: search.advance(away(2, 10), []), lambda: search.advance(z(2, 10), [away(2, 8)])):
         with pytest.raises(ValueError, match="must be on"):
             call()
+
+
+# ------------------------------------------------------------------------------------------
+# state arrays of the binding's reordering
+# ------------------------------------------------------------------------------------------
+@pytest.fixture
+def reorder(monkeypatch):
+    """fcm_beam_reorder of these pools, with the library's function stubbed: the (pool, slot bytes, slots)
+    it would be given."""
+    import depthwise_pointwise_convolution_amd as F
+    got = []
+
+    class Lib:
+        @staticmethod
+        def fcm_beam_reorder(prob, parent, slots, out, n, ptrs, bytes_, slots_, stream):
+            got.append([(ptrs[i], bytes_[i], slots_[i]) for i in range(n)])
+            return 0
+
+    monkeypatch.setattr(F, "lib", lambda: Lib)
+    return lambda *pools: (got.clear(), F.fcm_beam_reorder(None, 1, 2, 3, list(pools), stream=0), got[0])[2]
+
+
+def test_state_arrays_with_gaps_are_refused(reorder):
+    # a slot is as many bytes as slots are apart: with gaps in it, or before the first slot's start, the last
+    # slot's copy would end behind the array
+    base = z(6, 12)
+    for bad in (base[:, 4:], base[:, ::2], base.reshape(6, 3, 4)[:, :, :2], base.reshape(6, 3, 4)[:, 1:],
+                base[:, 8:].unsqueeze(1).expand(6, 3, 4), z(1, 12).expand(6, 12), base.t()[:, :5],
+                z(30).as_strided((4, 2, 2), (4, 3, 1))):
+        with pytest.raises(ValueError, match="slots"):
+            reorder(z(6, 4), bad)
+
+
+def test_state_arrays_without_gaps_are_taken(reorder):
+    base = z(6, 3, 4)
+    for good in (base, base[1:4], base.transpose(1, 2), base.reshape(6, 12)[2:], z(6, dtype=BF), base[:1],
+                 z(6, 1, 5, 1), z(6, 2, 3, 4).permute(0, 3, 1, 2)):
+        size = good[0].numel() * good.element_size()
+        assert reorder(good) == [(good.data_ptr(), size, good.shape[0])]
+    # the only slot of an array, whatever its distance to a next one
+    assert reorder(z(6, 12)[:1, :4])[0][1] == 16
