@@ -62,6 +62,11 @@ __device__ __forceinline__ void transpose_groups(uint32_t* w) {
 constexpr int kStep = 128;   // channels a wave takes at a time: 64 bytes of an output channel
 constexpr int kSpan = 8;      // steps whose scales a workgroup holds in LDS at a time
 
+// Byte offset in x of the channels behind the last, which read as zero: beyond every range of a
+// tile's tokens (31 row strides below 2^26 elements and 2^20 channels, 0xf8200000 bytes), and with a
+// step's own offset of up to 2^21 still below 2^32.
+constexpr uint32_t kBehind = 0xfc000000u;
+
 // A workgroup has 16 * RT output channels and 16 * MT tokens (or 4, 8: NI = 1, 2); its waves take
 // every NW-th step of 128 channels and add their sums through LDS.
 //
@@ -90,6 +95,7 @@ __global__ __launch_bounds__(64 * NW, (MT == 2 && RT == 2) || (GROUP == 32 && RT
     static_assert(kSpan % NW == 0, "a wave's steps are the same ones of every span");
     constexpr int XI = MT * NI;            // loads of 4 tokens
     constexpr int TOKENS = 4 * XI;
+    static_assert(TOKENS <= 32, "kBehind lies behind a tile's tokens");
     // a wave's steps pass through `stage`; its sums lie there at the end
     __shared__ u32x4 stage[NW][RT + XI][64];
     __shared__ float2 sz[SG][16 * RT];
@@ -141,7 +147,7 @@ __global__ __launch_bounds__(64 * NW, (MT == 2 && RT == 2) || (GROUP == 32 && RT
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
             uint32_t at = xat[i];
-            if (!WIDE && s * kStep + 8 * (sub ^ ((4 * i + grp) & 15)) >= a.C) at = mm::kOob;
+            if (!WIDE && s * kStep + 8 * (sub ^ ((4 * i + grp) & 15)) >= a.C) at = kBehind;
             v.x[i] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, s * kStep * 2, 0);
         }
     };

@@ -602,3 +602,26 @@ def test_example_decodes_and_its_scores_hold():
     worst = E.main(["--dim", "128", "--layers", "2", "--vocab", "501", "--requests", "3", "--beams", "4",
                     "--tokens", "12", "--check"])
     assert worst < 0.5
+
+
+# ------------------------------------------------------------------------------------------
+# large strides and values that are not finite
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("M,C,ldx,group", [(32, 136, 2 ** 25 + 2 ** 22, 32), (20, 1000, 2 ** 26 - 8, 128),
+                                           (18, 24, 2 ** 26 - 8, 64), (5, 136, 2 ** 26 - 8, 64)])
+def test_q4_rows_far_apart(M, C, ldx, group):
+    # a tile's rows span more than 2^31 bytes: channels behind the last are zero, whatever lies between the
+    # rows.  Whole numbers and scales that are powers of two: exact
+    import depthwise_pointwise_convolution_amd as F
+    g = _gen(C + M)
+    K = 40
+    v = _q4_inputs(g, "bf16", M, C, K, group, True)
+    x = torch.randint(-2, 3, (M, C), generator=g).to(torch.bfloat16)
+    scales = (2.0 ** torch.randint(-6, -2, v["scales"].shape, generator=g)).to(torch.bfloat16)
+    wide = torch.full(((M - 1) * ldx + C,), 512.0, dtype=torch.bfloat16, device="cuda").as_strided((M, C), (ldx, 1))
+    wide.copy_(x)
+    ref, _ = O.q4("bf16", x, v["q"], scales, v["zeros"], None, group, "none")
+    y = torch.full((M, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    F.fcm_q4_fwd(F.q4_problem("bf16", M, C, K, group=group, ldx=ldx), wide, v["q"].cuda(), scales.cuda(),
+                 v["zeros"].cuda(), None, y)
+    assert torch.equal(y.cpu(), ref.float().to(torch.bfloat16))
