@@ -230,9 +230,13 @@ __global__ __launch_bounds__(64 * NW, (MT == 2 && RT == 2) || (GROUP == 32 && RT
         if (s0) __syncthreads();
         for (int j = threadIdx.x; j < 16 * RT * SG; j += 64 * NW) {
             const int row = j / SG, g = s0 * GS + j % SG;
-            const uint32_t at = row < krows && g < groups ? row * groups + g : 0;
+            // (a step has places for groups behind the last: zero, or a scale that is not finite
+            // would meet their zero sums)
+            const bool in = row < krows && g < groups;
+            const uint32_t at = in ? row * groups + g : 0;
             const float z = a.zeros ? (float)(zero0[at] & 15) : 8.0f;
-            sz[j % SG][row] = float2{(float)scale0[at], -16.0f - z};
+            const float scale = (float)scale0[at];
+            sz[j % SG][row] = in ? float2{scale, -16.0f - z} : float2{};
         }
         __syncthreads();
         const int end = s0 + kSpan < steps ? s0 + kSpan : steps;

@@ -625,3 +625,21 @@ def test_q4_rows_far_apart(M, C, ldx, group):
     F.fcm_q4_fwd(F.q4_problem("bf16", M, C, K, group=group, ldx=ldx), wide, v["q"].cuda(), scales.cuda(),
                  v["zeros"].cuda(), None, y)
     assert torch.equal(y.cpu(), ref.float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("C,group", [(136, 32), (1000, 64), (264, 64)])
+def test_q4_scales_that_are_not_finite_stay_in_their_channel(C, group):
+    # groups that a last step of 128 channels has room for but C has not
+    import depthwise_pointwise_convolution_amd as F
+    g = _gen(C)
+    M, K = 5, 70
+    v = _q4_inputs(g, "bf16", M, C, K, group, True)
+    for k in range(0, K, 16):  # the first channel of every tile
+        v["scales"][k, 0] = float("inf") if k % 32 else float("nan")
+    y = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    F.fcm_q4_fwd(F.q4_problem("bf16", M, C, K, group=group), v["x"].cuda(), v["q"].cuda(), v["scales"].cuda(),
+                 v["zeros"].cuda(), None, y)
+    rest = [k for k in range(K) if k % 16]
+    ref, tol = O.q4("bf16", v["x"], v["q"][rest], v["scales"][rest], v["zeros"][rest], None, group, "none")
+    _within(y[:, rest], ref, tol, "channels with finite scales")
+    assert not y[:, ::16].isfinite().any()
