@@ -21,9 +21,11 @@ namespace fcm {
 namespace {
 
 // A in base 2.  A decay rate of -infinity is taken as the largest float: a step of zero then still
-// leaves the state alone (0 * infinity would be NaN).
+// leaves the state alone (0 * infinity would be NaN).  A rate that is NaN stays so (a maximum would
+// make it -FLT_MAX).
 __device__ __forceinline__ float rate2(float A) {
-    return __builtin_fmaxf(A * 1.44269504f, -FLT_MAX);
+    const float r = A * 1.44269504f;
+    return r < -FLT_MAX ? -FLT_MAX : r;
 }
 
 // A channel's N <= NP values: in 16-byte pieces (`wide`: N is a multiple of 4 and the array 16-byte

@@ -643,3 +643,22 @@ def test_q4_scales_that_are_not_finite_stay_in_their_channel(C, group):
     ref, tol = O.q4("bf16", v["x"], v["q"][rest], v["scales"][rest], v["zeros"][rest], None, group, "none")
     _within(y[:, rest], ref, tol, "channels with finite scales")
     assert not y[:, ::16].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype,N,lens", [("f32", 16, [3]), ("bf16", 16, [40, 0, 7]), ("f32", 5, [9, 2]), ("f16", 24, [70])])
+@pytest.mark.parametrize("step", [False, True])
+def test_a_rate_that_is_no_number_shows(dtype, N, lens, step):
+    # (a maximum with the lowest float would make a NaN weight forget and answer with finite values)
+    import depthwise_pointwise_convolution_amd as F
+    g = _gen(N)
+    lens = [1] * len(lens) if step else lens
+    B, T, cu, D = len(lens), sum(lens), _offsets(lens), 40
+    v = _scan_inputs(g, dtype, T, D, N, 1, B, B, False)
+    v["A"][7, N - 2] = float("nan")
+    y, state = _run_scan(F, v, dtype, cu, list(range(B)), [1] * B, 1, (0, 0, 0, 0), step=step)
+    other = [d for d in range(D) if d != 7]
+    assert y[:, 7].isnan().all() and y[:, other].isfinite().all()
+    ran = [b for b in range(B) if lens[b]]
+    assert state[ran, 7, N - 2].isnan().all()
+    state[ran, 7, N - 2] = 0
+    assert state.isfinite().all()
