@@ -199,10 +199,12 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a
     for (int tile = k.first; tile < k.end; tile += TILE) {
         const int rows = tile + TILE < k.end ? TILE : k.end - tile;
         __syncthreads();
-        for (int i = threadIdx.x; i < rows * NS; i += blockDim.x) {
+        // (up to whole turns, with zeros for the tokens behind the end)
+        const int filled = (rows + kTurn - 1) / kTurn * kTurn * NS;
+        for (int i = threadIdx.x; i < filled; i += blockDim.x) {
             const int t = i / NS, n = i % NS;
             const long long r = tile + t;
-            const bool in = n < a.N;
+            const bool in = n < a.N && t < rows;
             const T* b = (const T*)a.Bm + r * a.ldb + (long long)g * a.N + n;
             const T* cc = (const T*)a.Cm + r * a.ldc + (long long)g * a.N + n;
             float* to = (float*)bc[t];
@@ -216,10 +218,10 @@ __global__ __launch_bounds__(64 * kScanWaves, 4) void scan_fwd_kernel(ScanArgs a
             float outs[kTurn];
 #pragma unroll
             for (int i = 0; i < kTurn; ++i) {
-                // Tokens behind the end take a step of zero, which leaves the state as it is
-                // (their row of the tile is the last).
+                // Tokens behind the end take a step of zero on a B of zero, which leaves the state as
+                // it is.
                 const bool here = t0 + i < rows;
-                const f32x4* row = bc[here ? t0 + i : rows - 1] + n0 / 4;
+                const f32x4* row = bc[t0 + i] + n0 / 4;
                 const float xv = (float)xs[i];
                 const float v = (float)ds[i] + bias;
                 const float sp = softplus(v);

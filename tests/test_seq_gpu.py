@@ -662,3 +662,26 @@ def test_a_rate_that_is_no_number_shows(dtype, N, lens, step):
     assert state[ran, 7, N - 2].isnan().all()
     state[ran, 7, N - 2] = 0
     assert state.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,N", [("f32", 16), ("bf16", 8), ("f16", 24)])
+@pytest.mark.parametrize("lens", [[5, 3], [1], [0, 13, 6], [70, 2]])
+def test_an_infinite_state_stays_infinite(dtype, N, lens):
+    # the last row of a sequence is its only infinite one: nothing behind it may touch the state
+    import depthwise_pointwise_convolution_amd as F
+    g = _gen(N + len(lens))
+    B, T, cu, D = len(lens), sum(lens), _offsets(lens), 24
+    v = _scan_inputs(g, dtype, T, D, N, 1, B, B, False)
+    v["x"] = v["x"].abs() + 0.5
+    for b in range(B):
+        if lens[b]:
+            v["Bm"][cu[b + 1] - 1, N - 1] = math.inf if b % 2 else -math.inf
+    v["Cm"] = v["Cm"].abs() + 0.5
+    _, state = _run_scan(F, v, dtype, cu, list(range(B)), [1] * B, 1, (0, 0, 0, 0))
+    args = [v[k] for k in ("x", "dt", "A", "Bm", "Cm", "skip", "dt_bias", "z")]
+    _, _, sref, stol, _ = O.scan(dtype, *args, cu, list(range(B)), [1] * B, v["state"], 1, True)
+    far = sref.isinf()
+    assert far.any() and torch.equal(state.cpu().double()[far], sref[far])
+    stol[far], sref[far] = 0, 0
+    state[far.cuda()] = 0
+    _within(state, sref, stol, "the other states")
