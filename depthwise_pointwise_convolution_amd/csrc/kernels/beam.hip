@@ -203,11 +203,12 @@ __global__ __launch_bounds__(256, 8) void beam_rows_kernel(BeamArgs a, int split
 // one after the other, 3 us each: 31 against 9.7 us for 4 rows of 32000.)
 //
 // One workgroup per request.  A wave per beam (in turn): the splits' sums give the row's
-// log-sum-exp, and lane s walks split s's best tokens while the best head of all lanes is taken
+// log-sum-exp, kept as its largest logit and the log of the sum above that (beside 3e38, a mask of the
+// type's lowest value or an infinite logit, the log would be lost also in 64 bits), and lane s walks split s's best tokens while the best head of all lanes is taken
 // W times.  Then the first wave does the same over the beams, on scores in 64 bits.
 __global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits) {
     __shared__ Key rowbest[32][32];
-    __shared__ double rowlse[32];
+    __shared__ double rowtop[32], rowlog[32];
     constexpr int AHEAD = 4;  // of a split's tokens, loaded at once
     const int r = blockIdx.x, lane = threadIdx.x & 63, W = a.beams;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -229,7 +230,10 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits)
         double part = 0.0;
         if (head.top > -inf) part = (double)head.sum * exp((double)head.top - (double)top);
         part = wave_sum(part);
-        if (lane == 0) rowlse[w] = top > -inf ? (double)top + log(part) : -(double)inf;
+        if (lane == 0) {
+            rowtop[w] = top;
+            rowlog[w] = top > -inf ? log(part) : 0.0;
+        }
         int at = 0;
         Key cur = ahead[0];
         for (int i = 0; i < W; ++i) {
@@ -251,8 +255,8 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits)
     __syncthreads();
     if (wave != 0) return;
     const bool live = lane < W;
-    const double lse = rowlse[live ? lane : 0];
-    const bool dead = !(score > -inf) || !(lse > -(double)inf);
+    const double rtop = rowtop[live ? lane : 0], rlog = rowlog[live ? lane : 0];
+    const bool dead = !(score > -inf) || !(rtop > -(double)inf);
     int at = 0;  // tokens of this beam taken so far
     for (int k = 0; k < W; ++k) {
         double total = -(double)inf;
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(BeamArgs a, int splits)
                 const Key c = rowbest[lane][at];
                 tok = c != 0 ? key_token(c) : -1;
                 const float l = key_logit(c);
-                if (tok >= 0 && l > -inf) total = (double)score + ((double)l - lse);
+                if (tok >= 0 && l > -inf) total = (double)score + (((double)l - rtop) - rlog);
             }
         }
         // the largest total, then the lowest place in beams x vocabulary

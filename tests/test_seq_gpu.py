@@ -685,3 +685,28 @@ def test_an_infinite_state_stays_infinite(dtype, N, lens):
     stol[far], sref[far] = 0, 0
     state[far.cuda()] = 0
     _within(state, sref, stol, "the other states")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("W,V", [(3, 50), (4, 3000), (2, 40000)])
+def test_beams_over_rows_of_extreme_values(dtype, W, V):
+    # a row that is masked with the type's lowest value altogether is V equal tokens, one with two infinite
+    # logits is two: their log-sum-exps differ from those values by log V and log 2, which a sum beside
+    # 3e38 loses also in 64 bits
+    import depthwise_pointwise_convolution_amd as F
+    t = O.TYPES[dtype]
+    g = _gen(V)
+    R = 3
+    logits = torch.randn(R * W, V, generator=g).to(t)
+    logits[0] = torch.finfo(t).min
+    logits[W + 1, [2, V - 1]] = math.inf
+    logits[2 * W:] = torch.finfo(t).min
+    scores = -0.1 - torch.arange(R * W).float() / 64
+    _, nxt, par, tok, _ = _run_beam(F, dtype, logits, scores, None, R, W, -1)
+    l = logits.double().clamp(max=torch.finfo(torch.float32).max)
+    top = l.max(-1, keepdim=True).values
+    logp = (l - top) - torch.log(torch.exp(l - top).sum(-1, keepdim=True))
+    best, at = torch.sort((scores.double()[:, None] + logp).reshape(R, W * V), descending=True, stable=True)
+    best, at = best[:, :W].reshape(-1), at[:, :W].reshape(-1)
+    assert par.tolist() == (at // V).tolist() and tok.tolist() == (at % V).tolist()
+    assert ((nxt.double() - best).abs() <= 2.0 ** -20 + 2.0 ** -23 * best.abs()).all()
