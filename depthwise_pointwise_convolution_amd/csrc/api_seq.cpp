@@ -178,6 +178,8 @@ fcm_status check_beam(const fcm_beam_problem* p) {
         return invalid("beams and vocab must be positive, requests not negative");
     if (p->beams > 32) return unsupported("more than 32 beams of a request");
     if (p->eos < -1 || p->eos >= p->vocab) return invalid("eos must be -1 or a token");
+    // (the selection's places reach up to a split, vocab / 64, behind the vocabulary)
+    if (p->vocab > INT_MAX - (1 << 25) + 1) return unsupported("vocab above 2^31 - 2^25");
     if ((long long)p->beams * p->vocab > INT_MAX) return unsupported("beams * vocab above 2^31-1");
     if ((long long)p->requests * p->beams > (1 << 24)) return unsupported("requests * beams above 2^24");
     return FCM_OK;

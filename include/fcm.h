@@ -516,7 +516,7 @@ typedef struct {
     int32_t dtype;    /* FCM_F32, FCM_F16 or FCM_BF16: logits */
     int32_t requests; /* independent searches */
     int32_t beams;    /* beams of a request, 1 to 32 */
-    int32_t vocab;
+    int32_t vocab;    /* up to 2^31 - 2^25, beams * vocab up to 2^31 - 1 */
     int32_t eos;      /* token that ends a beam; -1: none */
     int64_t ldl;      /* row stride of the logits */
 } fcm_beam_problem;

@@ -242,3 +242,18 @@ def test_wrappers_refuse_wrong_shapes_and_types():
                 lambda: BeamSearch(1, 2, 10, z(2, dtype=torch.int32)).advance(z(3, 10), [])):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_a_vocabulary_whose_places_overflow_is_refused():
+    # a row is cut into 64 splits at most, of whole blocks of 1024 tokens, so places up to a split
+    # and a block behind the vocabulary are computed in 32 bits
+    F = _F()
+    most = 2 ** 31 - 2 ** 25
+    per = -(-(-(-most // 1024)) // 64) * 1024  # tokens of a split
+    assert most + per - 1 < 2 ** 31 and -(-most // per) * per + 1024 < 2 ** 31
+    assert F.fcm_beam_workspace(F.beam_problem("f16", 1, 1, most)) == -(-most // per) * (8 + 8)
+    for vocab in (most + 1, 2 ** 31 - 2 ** 16, 2 ** 31 - 1):
+        prob = F.beam_problem("f16", 1, 1, vocab)
+        _refused(lambda: F.fcm_beam_select(prob, *[BASE] * 8, stream=0), 2, "vocab")
+        with pytest.raises(F.FcmError):
+            F.fcm_beam_workspace(prob)
