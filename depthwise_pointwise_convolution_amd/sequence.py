@@ -294,8 +294,10 @@ class BeamSearch:
 
     def advance(self, logits: torch.Tensor, pools: Sequence[torch.Tensor], stream=None):
         """Takes the logits [requests*beams, vocab] of the beams' last tokens, picks the next beams,
-        and moves the states in `pools` ([slots, ...], contiguous) to them.  Returns (parent, token);
-        scores, done and slots are the new beams'."""
+        and moves the states in `pools` ([slots, ...], contiguous) to them.  Returns (parent, token),
+        tensors of this step's own, to trace the beams back by; scores, done and slots are the new beams'
+        (two sets of buffers in turn, so that two steps can be captured and replayed as one graph: the
+        call after the next writes over them)."""
         if stream is not None:
             return _on(stream, lambda: self.advance(logits, pools), logits, *pools)
         n = self.requests * self.beams
@@ -312,6 +314,7 @@ class BeamSearch:
             self._ws = torch.empty(max(16, fcm_beam_workspace(prob)), dtype=torch.uint8,
                                    device=logits.device)
         scores, done, slots = self._next
+        self.parent, self.token = torch.empty(2, n, dtype=torch.int32, device=slots.device).unbind()
         fcm_beam_select(prob, logits, self.scores, self.done if self.eos >= 0 else None, self._ws,
                         scores, self.parent, self.token, done)
         for i in range(0, len(pools), 8) or (0,):

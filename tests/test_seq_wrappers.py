@@ -305,3 +305,28 @@ def test_state_arrays_without_gaps_are_taken(reorder):
         assert reorder(good) == [(good.data_ptr(), size, good.shape[0])]
     # the only slot of an array, whatever its distance to a next one
     assert reorder(z(6, 12)[:1, :4])[0][1] == 16
+
+
+# ------------------------------------------------------------------------------------------
+# a search's results
+# ------------------------------------------------------------------------------------------
+def test_each_step_of_a_search_has_its_own_results(calls, monkeypatch):
+    # parents and tokens are what a caller keeps of every step to trace the beams back by
+    step = iter(range(1, 9))
+
+    def select(prob, logits, scores, done, ws, nxt, parent, token, next_done, *stream):
+        n = next(step)
+        nxt.fill_(-n), parent.fill_(n), token.fill_(10 * n), next_done.fill_(n)
+
+    def reorder(prob, parent, slots, next_slots, pools, *stream):
+        next_slots.copy_(slots + 1)
+
+    monkeypatch.setattr(S, "fcm_beam_select", select)
+    monkeypatch.setattr(S, "fcm_beam_reorder", reorder)
+    search = S.BeamSearch(1, 2, 10, ints(0, 1), eos=3)
+    kept = [(search.advance(z(2, 10), [z(4, 8)]), search.scores, search.done, search.slots) for _ in range(4)]
+    for n, ((parent, token), _, _, _) in enumerate(kept, 1):
+        assert parent.tolist() == [n] * 2 and token.tolist() == [10 * n] * 2
+    for n, (_, scores, done, slots) in list(enumerate(kept, 1))[-2:]:
+        assert scores.tolist() == [-n] * 2 and done.tolist() == [n] * 2 and slots.tolist() == [n, n + 1]
+    assert search.parent is kept[-1][0][0] and search.token is kept[-1][0][1]

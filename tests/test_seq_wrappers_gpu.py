@@ -71,3 +71,62 @@ def test_broadcast_rows_give_what_their_copies_give():
     pools = [torch.randn(4, 8, generator=g).cuda()]
     a, b = one.advance(y[:1].expand(4, 500), pools), all_.advance(y[:4], [pools[0].clone()])
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and torch.equal(one.scores, all_.scores)
+
+
+def test_beams_traced_back_by_the_steps_results():
+    # the tokens of every beam, gathered step by step and from the kept parents and tokens at the end
+    import depthwise_pointwise_convolution_amd.sequence as S
+    g = torch.Generator().manual_seed(4)
+    R, W, V, steps = 2, 3, 300, 6
+    search = S.BeamSearch(R, W, V, torch.arange(R * W, dtype=torch.int32).cuda())
+    base = torch.arange(R).repeat_interleave(W).cuda() * W
+    history, kept = torch.zeros(R * W, 0, dtype=torch.int32).cuda(), []
+    for _ in range(steps):
+        parent, token = search.advance(torch.randn(R * W, V, generator=g).cuda(), [])
+        history = torch.cat([history[base + parent], token[:, None]], 1)
+        kept.append((parent, token))
+    at = torch.arange(R * W).cuda()
+    back = []
+    for parent, token in reversed(kept):
+        back.insert(0, token[at])
+        at = base[at] + parent[at]
+    assert torch.equal(torch.stack(back, 1), history)
+
+
+def test_a_block_and_a_search_in_a_graph():
+    # two steps (the search's buffers alternate) captured and replayed, against the same steps run eagerly
+    import depthwise_pointwise_convolution_amd.sequence as S
+    g = torch.Generator().manual_seed(5)
+    W, V = 3, 200
+    x = torch.randn(W, 128, generator=g).to(BF).cuda()
+    head = _linear(S, g, 128, V)
+    slots = torch.arange(W, dtype=torch.int32).cuda()
+
+    def start():
+        return _block(S, slots=W), S.BeamSearch(1, W, V, slots)
+
+    def two(b, search):
+        out = []
+        for _ in range(2):
+            out += list(search.advance(head(b.step(x, search.slots)), [b.window, b.state]))
+        return out
+
+    b, search = start()
+    want = []
+    for _ in range(4):
+        out = two(b, search)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out + [search.scores, search.slots, b.state]])
+    b, search = start()
+    two(b, search)  # (the workspace and the kernels are there before the capture)
+    torch.cuda.synchronize()
+    fresh, fresh_search = start()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = two(fresh, fresh_search)
+    for k in range(4):
+        graph.replay()
+        (torch.ones(1000, device="cuda") * 2).sum().item()
+        torch.cuda.synchronize()
+        for i, (a, c) in enumerate(zip(out + [fresh_search.scores, fresh_search.slots, fresh.state], want[k])):
+            assert torch.equal(a, c), (k, i)
