@@ -2,8 +2,10 @@
 // and the reordering of the beams' states.
 //
 // Both are readings of memory.  On MI355X, 32 requests of 8 beams over 65537 fp32 logits: the rows
-// 25 us (67 MB, 2.7 TB/s: instruction issue, the vector units busy 45% of the time beside the waits
-// of the cross-lane steps; 16 or 32 tokens a lane, one block or several a wave take 25 to 29 us),
+// 25 us (67 MB, 2.7 TB/s.  Neither the bytes nor issue bounds them, the vector units are busy 45% of the
+// time: a wave loads a block, takes W maxima one after the other, and only then loads the next; half of
+// its life it waits for such results, a third for its turn to issue.  16 or 32 tokens a lane, one block
+// or several a wave take 25 to 29 us),
 // the merge 8.5 us (a chain of latencies), the copies of 158 states of 1.1 MB 52 us (7 TB/s, part of
 // it from the Infinity Cache).  One request of 4 beams over 32000 fp16 logits: 4.6, 5 and 4 us.
 #include <float.h>

@@ -1,11 +1,12 @@
 // q4.hip -- pointwise layer with 4-bit weights and group scales for a few tokens:
 //   y[m][k] = act(bias[k] + sum_groups scale[k][g] * sum_{c in g} (q[k][c] - zero[k][g]) x[m][c]).
 //
-// The weights are read once, so the bytes of q bound it up to a few dozen tokens; the products run
-// on the matrix cores, where the spare tokens of a 16-row tile cost nothing.  On MI355X, 65536 x
-// 4096: one token 30 us (4.6 TB/s of codes and scales), 16 tokens with groups of 64 38.8 us (3.7
+// A tile of tokens, 32 at most, reads the weights once, and the bytes of q are its floor; the products
+// run on the matrix cores, where the spare tokens of a 16-row tile cost nothing.  On MI355X, 65536 x
+// 4096: one token 28 us (4.9 TB/s of codes and scales), 16 tokens with groups of 64 39 us (3.7
 // TB/s; vector units busy 42% of the time with unpacking and scales, the loads take turns with
-// them); 8192 x 2048 for one token 4.5 us, most of it launch and one memory latency.
+// them), 32 tokens 64 us (the products' and scales' work for each 16); 8192 x 2048 for one token 4.2 us,
+// most of it launch and one memory latency.  More tokens than 32 read and unpack the weights again.
 #include "mm_common.h"
 #include "seq_common.h"
 #include "../seq.h"

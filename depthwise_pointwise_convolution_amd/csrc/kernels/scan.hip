@@ -6,9 +6,10 @@
 // multiply-adds, about 130 slots with N = 16 against 8 bytes: the vector units bound it.  The
 // recurrence leaves D * seqs independent chains, too few for 1024 SIMDs, so long sequences are cut
 // into chunks and scanned twice, 11/6 of the work.  On MI355X: eleven prompts, 8192 tokens x 4096
-// fp16 channels in all, N = 16: 239 us (first pass 100, join 17, second pass 130; a pass without
-// the cut would take 110 at the vector units' peak, the bytes 53); one prompt of 2048 x 2048 bf16:
-// 51 us.  In both passes the vector units are busy 84% of the time (counters).
+// fp16 channels in all, N = 16: 238 us (in a kernel trace, where kernels do not overlap and each is a
+// little slower, first pass 99, join 17, second pass 135; a pass without the cut would take 110 at the
+// vector units' peak, the bytes 53); one prompt of 2048 x 2048 bf16: 51 us (20, 9 and 23).  For the
+// eleven prompts the vector units are busy 86% of the first and 85% of the second pass (counters).
 //
 // One token: the fp32 state is read and written, 8 N bytes a channel: HBM bounds it.  256 tokens x
 // 4096 channels: 26 us, 5.5 TB/s.
@@ -449,8 +450,10 @@ long long token_waves(int tokens, int D, int groups) {
 // us with 8 / 16 / 32 / 64 / 128 tokens, 16 states, bf16:
 //   512 x 1024: 27 / 29 / 38 / 59 / 102, 512 x 4096: 40 / 35 / 40 / 60 / 102,
 //   2048 x 2048: 76 / 59 / 54 / 65 / 107, 8192 x 4096: 425 / 291 / 237 / 221 / 232.
-// One thread goes along a sequence's chunks to join them, so a long sequence has no more than 256:
-// 16000 x 256 takes 87 us with 32 and 80 with 64.
+// One thread goes along a sequence's chunks to join them, so there are no more than 256 a sequence:
+// 16000 x 256 takes 87 us with 32 tokens and 80 with 64.  That is of all sequences together (the host
+// does not know their lengths): 8000 x 64 takes 43 us as one sequence and as four equal ones, but 109
+// us as one of 7997 tokens beside three short ones, whose thousand chunks one thread joins.
 int chunk_len(int tokens, int seqs, int D, int groups) {
     const long long w = token_waves(tokens, D, groups);
     int len = w < 2 ? 8 : w < 12 ? 16 : w < 48 ? 32 : 64;

@@ -56,7 +56,8 @@ __device__ __forceinline__ float silu(float v) {
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) <= 1.  u = 1 + e loses the low bits of
 // a small e; what it lost, e - (u - 1), is exact and is added back to log(u), whose slope there
-// is 1 to within e: the result keeps a relative error of a few 2^-24 down to the smallest v.
+// is 1 to within e.  The exponential's argument is rounded: far below zero, where the result is e, its
+// relative error is about (3 + 1.5 |v|) 2^-24, and below -87.3, where e would be subnormal, it is zero.
 __device__ __forceinline__ float softplus(float v) {
     const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(v) * -1.44269504f);
     const float u = 1.0f + e;

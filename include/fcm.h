@@ -460,7 +460,8 @@ fcm_status fcm_dw1d_step(const fcm_dw1d_problem* prob, const void* x, const void
  *   delta = dt[t][d] + dt_bias[d], through softplus(v) = log(1 + exp(v)) if `softplus`
  *   h[d][n] = exp(delta * A[d][n]) * h[d][n] + delta * Bm[t][g][n] * x[t][d]
  *   y[t][d] = (sum_n Cm[t][g][n] * h[d][n] + skip[d] * x[t][d]) * (z ? z * sigmoid(z) : 1)
- * A <= 0 keeps the recurrence bounded. */
+ * A <= 0 keeps the recurrence bounded (-infinity: any step but zero forgets).  A state that has
+ * become infinite may be NaN later in its sequence, whose chunks' decays are multiplied up first. */
 typedef struct {
     int32_t dtype;    /* FCM_F32, FCM_F16 or FCM_BF16: x, dt, Bm, Cm, z, y */
     int32_t D, N;     /* channels; states of a channel, 1 to 64 */
@@ -497,7 +498,9 @@ fcm_status fcm_scan_step(const fcm_scan_problem* prob, const void* x, const void
  * [K][ceil(C/group)] in the storage type; zeros: [K][ceil(C/group)] uint8 in 0..15, or NULL
  * for 8 throughout (the low four bits are used); bias: [K] fp32 or NULL; x: [M][C];
  * y: [M][K].  The last group may be short.  The arrays are read as they are: nothing is
- * packed.  Products are exact and summed in fp32; only y is rounded. */
+ * packed.  Products are exact and summed in fp32; only y is rounded.  The codes are read as
+ * 16 + q and the offset is taken off afterwards, so a token with an infinite value, or one whose
+ * 31 * sum |x| over a group passes the largest float, has outputs that are infinite or NaN. */
 typedef struct {
     int32_t dtype;   /* FCM_F16 or FCM_BF16: x, scales, y */
     int32_t M, C, K; /* tokens; input channels, a multiple of 8; output channels */
