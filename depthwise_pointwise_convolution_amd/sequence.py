@@ -236,7 +236,7 @@ class StateSpaceBlock:
         self._index(slots, B, "slots")
         self._index(carry, B, "carry")
         xs, z = self._halves(x)
-        u = torch.empty(T, self.inner, dtype=self.dtype, device=x.device)
+        u = torch.empty(T, self.inner, dtype=self.dtype, device=self.window.device)
         fcm_dw1d_fwd(dw1d_problem(self.name, self.inner, self.W, tokens=T, seqs=B,
                                   slots=self.slots, ldx=_stride(xs)),
                      xs, self.conv_w, self.conv_b, cu, slots, carry, self.window, u)
@@ -244,7 +244,8 @@ class StateSpaceBlock:
         y = torch.empty_like(u)
         prob = scan_problem(self.name, self.inner, self.N, tokens=T, seqs=B, slots=self.slots,
                             lddt=_stride(dt), ldb=_stride(b), ldc=_stride(c), ldz=_stride(z))
-        ws = torch.empty(max(16, fcm_scan_workspace(prob)), dtype=torch.uint8, device=x.device)
+        ws = torch.empty(max(16, fcm_scan_workspace(prob)), dtype=torch.uint8,
+                         device=self.window.device)
         fcm_scan_fwd(prob, u, dt, self.A, b, c, self.skip, self.dt_bias, z, cu, slots, carry,
                      self.state, ws, y)
         return self.out_proj(y)
@@ -257,7 +258,7 @@ class StateSpaceBlock:
         B = x.shape[0]
         self._index(slots, B, "slots")
         xs, z = self._halves(x)
-        u = torch.empty(B, self.inner, dtype=self.dtype, device=x.device)
+        u = torch.empty(B, self.inner, dtype=self.dtype, device=self.window.device)
         fcm_dw1d_step(dw1d_problem(self.name, self.inner, self.W, tokens=B, seqs=B,
                                    slots=self.slots, ldx=_stride(xs)),
                       xs, self.conv_w, self.conv_b, slots, self.window, u)

@@ -14,9 +14,6 @@ BF = torch.bfloat16
 class Calls(list):
     """(name, problem, pointer arguments, stream) of the launches."""
 
-    def names(self):
-        return [c[0] for c in self]
-
 
 @pytest.fixture
 def calls(monkeypatch):
@@ -330,3 +327,13 @@ def test_each_step_of_a_search_has_its_own_results(calls, monkeypatch):
     for n, (_, scores, done, slots) in list(enumerate(kept, 1))[-2:]:
         assert scores.tolist() == [-n] * 2 and done.tolist() == [n] * 2 and slots.tolist() == [n, n + 1]
     assert search.parent is kept[-1][0][0] and search.token is kept[-1][0][1]
+
+
+def test_intermediates_lie_beside_the_states(calls):
+    # an in-projection that also moves its input: what the kernels write is not where that input is
+    x = torch.empty(2, 24, dtype=BF, device="meta")
+    b = block(in_proj=_gives(z(2, 32, dtype=BF)))
+    b.step(x, ints(0, 1))
+    b.prompt(x, ints(0, 2), ints(0))
+    for name, _, args, _ in calls:
+        assert all(a is None or a.device.type == "cpu" for a in args), name
