@@ -36,19 +36,27 @@ def _on_gpu(t: torch.Tensor) -> bool:
     return t.is_cuda and t.get_device() == torch.cuda.current_device()
 
 
+# (The checks of every step write their messages only where they refuse: a formatted shape or device
+# costs as much as the rest of a check.)
 def _beside(t: torch.Tensor, device: torch.device, name: str):
     """(a kernel that is given an address of another device, or of the host, faults)"""
-    _need(t.device == device, f"{name} must be on {device}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
 
 
 def _rows(t: torch.Tensor, width: int, dtype: torch.dtype, name: str, device: torch.device):
-    _beside(t, device, name)
-    _need(t.dim() == 2 and t.shape[1] == width, f"{name} must be [rows, {width}]")
-    _need(t.dtype == dtype, f"{name} must be {dtype}")
-    _need(t.shape[0] <= 1 or t.stride(1) == 1, f"{name}'s channels must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} must be [rows, {width}]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    one, (apart, step) = shape[0] <= 1, t.stride()
+    if step != 1 and not one:
+        raise ValueError(f"{name}'s channels must be contiguous")
     # (rows that overlap, as a broadcast one does, have no row stride that the library takes)
-    apart = t.shape[0] <= 1 or t.stride(0) >= width
-    return t if apart and (width == 1 or t.stride(1) == 1) else t.contiguous()
+    return t if (one or apart >= width) and (step == 1 or width == 1) else t.contiguous()
 
 
 def _out(t: torch.Tensor, rows: int, width: int, dtype: torch.dtype, device: torch.device):
@@ -68,7 +76,7 @@ def _stride(t: torch.Tensor) -> int:
 
 def _on(stream, call, *tensors):
     """`call` with all its work on `stream`.  The allocator hands memory out by stream: what `call`
-    makes belongs to `stream`, the caller's `tensors` may be freed while it still uses them, and so may the
+    makes belongs to `stream` (which has to outlive it), the caller's `tensors` may be freed while it still uses them, and so may the
     results while the current stream does; each is told of the other."""
     if not hasattr(stream, "wait_stream"):  # a raw handle, 0 the default stream's
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
@@ -200,14 +208,14 @@ class StateSpaceBlock:
 
     def _projected(self, p, rows: int, width: int, name: str):
         """What a projection gave, in the form the kernels take its rows."""
-        name = f"{name}'s result"
         p = _rows(p, width, self.dtype, name, self.window.device)
-        _need(p.shape[0] == rows, f"{name} must have {rows} rows")
+        if p.shape[0] != rows:
+            raise ValueError(f"{name} must have {rows} rows")
         return p
 
     def _halves(self, x):
         """(scan input, gate): the in-projection's two halves."""
-        xz = self._projected(self.in_proj(x), x.shape[0], 2 * self.inner, "in_proj")
+        xz = self._projected(self.in_proj(x), x.shape[0], 2 * self.inner, "in_proj's result")
         return xz[:, :self.inner], xz[:, self.inner:]
 
     def _parts(self, u):
@@ -215,15 +223,16 @@ class StateSpaceBlock:
         p = self.x_proj(u)
         _need(p.dim() == 2 and p.shape[1] > 2 * self.N, "x_proj must give the step's rows and then B and C")
         rank = p.shape[1] - 2 * self.N
-        p = self._projected(p, u.shape[0], p.shape[1], "x_proj")
-        dt = self._projected(self.dt_proj(p[:, :rank]), u.shape[0], self.inner, "dt_proj")
+        p = self._projected(p, u.shape[0], p.shape[1], "x_proj's result")
+        dt = self._projected(self.dt_proj(p[:, :rank]), u.shape[0], self.inner, "dt_proj's result")
         return dt, p[:, rank:rank + self.N], p[:, rank + self.N:]
 
     def _index(self, t, n: int, name: str):
-        if t is not None:
-            _beside(t, self.window.device, name)
-        _need(t is None or (t.dtype == torch.int32 and tuple(t.shape) == (n,) and t.is_contiguous()),
-              f"{name} must be [{n}] int32")
+        if t is None:
+            return
+        _beside(t, self.window.device, name)
+        if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be [{n}] int32")
 
     def prompt(self, x, cu, slots, carry=None, stream=None) -> torch.Tensor:
         """x: [tokens, dim], sequence b in rows cu[b] .. cu[b+1]-1 and state slot slots[b]; with
@@ -292,6 +301,7 @@ class BeamSearch:
         self._next = (torch.empty_like(self.scores), torch.empty_like(self.done),
                       torch.empty_like(self.slots))
         self._ws: Optional[torch.Tensor] = None
+        self._key = self._prob = None  # the last logits' form and their problem
 
     def advance(self, logits: torch.Tensor, pools: Sequence[torch.Tensor], stream=None):
         """Takes the logits [requests*beams, vocab] of the beams' last tokens, picks the next beams,
@@ -305,17 +315,21 @@ class BeamSearch:
         _need(logits.dtype in DTYPE_NAMES, "logits must be float32, float16 or bfloat16")
         _need(_on_gpu(self.slots), "the search must be on the current GPU")
         logits = _rows(logits, self.vocab, logits.dtype, "logits", self.slots.device)
-        _need(logits.shape[0] == n, f"logits must have {n} rows")
+        if logits.shape[0] != n:
+            raise ValueError(f"logits must have {n} rows")
         for p in pools:
             _beside(p, logits.device, "a state pool")
             _need(p.is_contiguous(), "state pools must be contiguous")
-        prob = beam_problem(DTYPE_NAMES[logits.dtype], self.requests, self.beams, self.vocab,
-                            eos=self.eos, ldl=_stride(logits))
+        key = (logits.dtype, self.eos, _stride(logits))
+        if key != self._key:
+            self._key, self._prob = key, beam_problem(DTYPE_NAMES[logits.dtype], self.requests, self.beams,
+                                                      self.vocab, eos=self.eos, ldl=key[2])
+        prob = self._prob
         if self._ws is None:
             self._ws = torch.empty(max(16, fcm_beam_workspace(prob)), dtype=torch.uint8,
                                    device=logits.device)
         scores, done, slots = self._next
-        self.parent, self.token = torch.empty(2, n, dtype=torch.int32, device=slots.device).unbind()
+        self.parent, self.token = torch.empty_like(slots), torch.empty_like(slots)
         fcm_beam_select(prob, logits, self.scores, self.done if self.eos >= 0 else None, self._ws,
                         scores, self.parent, self.token, done)
         for i in range(0, len(pools), 8) or (0,):
