@@ -24,6 +24,8 @@ fcm_status done(int rc) {
         if (_s != FCM_OK) return _s;   \
     } while (0)
 
+constexpr long long kThreads = 1ll << 32;  // a launch has fewer
+
 int elem(int dtype) { return dtype == FCM_F32 ? 4 : 2; }
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
@@ -336,6 +338,8 @@ fcm_status fcm_beam_select(const fcm_beam_problem* prob, const void* logits,
     a.beams = prob->beams;
     a.vocab = prob->vocab;
     a.eos = prob->eos;
+    if (beam_rows_threads(*prob) >= kThreads)
+        return unsupported("too large requests * beams * vocab for one launch");
     return done(launch_beam_select(a, prob->dtype, stream));
 }
 
@@ -369,6 +373,8 @@ fcm_status fcm_beam_reorder(const fcm_beam_problem* prob, const int32_t* parent,
     a.npools = npools;
     a.requests = prob->requests;
     a.beams = prob->beams;
+    if (beam_reorder_threads(a) >= kThreads)
+        return unsupported("more than 2^24 pieces of 16 KB in all beams' states");
     return done(launch_beam_reorder(a, stream));
 }
 

@@ -372,6 +372,10 @@ long long beam_workspace_bytes(const fcm_beam_problem& p) {
     return (long long)p.requests * p.beams * row_splits(p.vocab) * split_bytes(p.beams);
 }
 
+long long beam_rows_threads(const fcm_beam_problem& p) {
+    return ((long long)p.requests * p.beams * row_splits(p.vocab) + 3) / 4 * 256;
+}
+
 int launch_beam_select(const BeamArgs& a, int dtype, void* stream) {
     hipStream_t s = (hipStream_t)stream;
     const int splits = row_splits(a.vocab), blocks = split_blocks(a.vocab);
@@ -389,13 +393,21 @@ int launch_beam_select(const BeamArgs& a, int dtype, void* stream) {
     return (int)hipGetLastError();
 }
 
-int launch_beam_reorder(const ReorderArgs& a, void* stream) {
+namespace {
+long long reorder_chunks(const ReorderArgs& a) {
     long long chunks = 0;
     for (int q = 0; q < a.npools; ++q) chunks += (a.bytes[q] + kChunk - 1) / kChunk;
-    if (chunks == 0) chunks = 1;
-    const long long grid = chunks * a.requests * a.beams;
-    if (grid > INT_MAX) return (int)hipErrorInvalidConfiguration;
-    beam_reorder_kernel<<<(int)grid, 256, 0, (hipStream_t)stream>>>(a, (int)chunks);
+    return chunks > 0 ? chunks : 1;
+}
+}  // namespace
+
+long long beam_reorder_threads(const ReorderArgs& a) {
+    return reorder_chunks(a) * a.requests * a.beams * 256;
+}
+
+int launch_beam_reorder(const ReorderArgs& a, void* stream) {
+    const int chunks = (int)reorder_chunks(a);
+    beam_reorder_kernel<<<chunks * a.requests * a.beams, 256, 0, (hipStream_t)stream>>>(a, chunks);
     return (int)hipGetLastError();
 }
 

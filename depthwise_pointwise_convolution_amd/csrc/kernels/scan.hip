@@ -441,9 +441,11 @@ __global__ __launch_bounds__(256) void scan_step4_kernel(ScanArgs a, int cblocks
     }
 }
 
+// Waves of one chunk at 64 channels each.
+long long chunk_waves(int D, int groups) { return (long long)((D / groups + 63) / 64) * groups; }
 // Waves the scan would have if each took 64 channels of one token, in 4096ths.
 long long token_waves(int tokens, int D, int groups) {
-    return (long long)tokens * ((D / groups + 63) / 64) * groups / 4096;
+    return tokens * chunk_waves(D, groups) / 4096;
 }
 
 // Tokens of a chunk: short ones bring waves for a small batch, long ones hand on fewer states.
@@ -457,7 +459,10 @@ long long token_waves(int tokens, int D, int groups) {
 int chunk_len(int tokens, int seqs, int D, int groups) {
     const long long w = token_waves(tokens, D, groups);
     int len = w < 2 ? 8 : w < 12 ? 16 : w < 48 ? 32 : 64;
-    while (tokens / len > 256ll * (seqs > 0 ? seqs : 1) || tokens / len * (D / 64 + 1ll) > (1 << 24))
+    // Nor more than 2^23 waves for them (four times that where a channel has four lanes; the one chunk at
+    // least of every sequence adds up to 2^25): a launch has fewer than 2^32 threads.
+    while (len < (1 << 30) && (tokens / len > 256ll * (seqs > 0 ? seqs : 1) ||
+                               tokens / len * chunk_waves(D, groups) > (1 << 23)))
         len *= 2;
     return len;
 }

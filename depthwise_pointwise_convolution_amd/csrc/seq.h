@@ -76,6 +76,7 @@ struct BeamArgs {
 };
 int launch_beam_select(const BeamArgs& a, int dtype, void* stream);
 long long beam_workspace_bytes(const fcm_beam_problem& p);
+long long beam_rows_threads(const fcm_beam_problem& p);
 
 struct ReorderArgs {
     const int32_t* parent;
@@ -87,5 +88,6 @@ struct ReorderArgs {
     int npools, requests, beams;
 };
 int launch_beam_reorder(const ReorderArgs& a, void* stream);
+long long beam_reorder_threads(const ReorderArgs& a);
 
 }  // namespace fcm

@@ -257,3 +257,29 @@ def test_a_vocabulary_whose_places_overflow_is_refused():
         _refused(lambda: F.fcm_beam_select(prob, *[BASE] * 8, stream=0), 2, "vocab")
         with pytest.raises(F.FcmError):
             F.fcm_beam_workspace(prob)
+
+
+@pytest.mark.parametrize("T,B,D,N,G", [(1 << 24, 4096, 1 << 12, 1, 1 << 12), (1 << 24, 1 << 15, 1 << 10, 4, 1 << 9),
+                                       (1 << 29, 1 << 19, 64, 1, 64), (1 << 26, 1 << 15, 256, 64, 1),
+                                       (1 << 20, 1 << 11, 1 << 14, 16, 1), (1 << 22, 1, 1 << 12, 1, 1 << 12)])
+def test_a_scan_of_any_size_is_a_launch(T, B, D, N, G):
+    # a launch has fewer than 2^32 threads: 64 at least for each chunk of a channel group, at most four
+    # lanes a channel
+    F = _F()
+    size = F.fcm_scan_workspace(F.scan_problem("bf16", D, N, groups=G, tokens=T, seqs=B))
+    chunks, rest = divmod(size, (N + 1) * D * 4)
+    lanes = 1 if N <= 16 else 2 if N <= 32 else 4
+    assert rest == 0 and chunks * G * -(-(D // G) * lanes // 64) * 64 < 2 ** 32
+
+
+def test_launches_past_2_to_the_32_threads_are_refused():
+    F = _F()
+    # selection: a wave for each split of at least 1024 tokens
+    prob = F.beam_problem("f16", 1 << 20, 1, 1 << 16, eos=1)
+    _refused(lambda: F.fcm_beam_select(prob, *[BASE] * 8, stream=0), 2, "requests * beams * vocab")
+    prob = F.beam_problem("f16", (1 << 20) - 1, 1, 1 << 16)
+    assert F.fcm_beam_workspace(prob) == ((1 << 20) - 1) * 64 * 16
+    # reordering: 256 threads for each 16 KB of each beam's states
+    prob = F.beam_problem("f16", 1 << 10, 8, 100)
+    pool = _Pool(BASE, 4, 1 << 23)
+    _refused(lambda: F.fcm_beam_reorder(prob, BASE, BASE, 2 * BASE, [pool], stream=0), 2, "states")
