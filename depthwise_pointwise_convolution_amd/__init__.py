@@ -17,7 +17,11 @@ and the sequence operators, each on its own small problem descriptor:
 
     fcm_dw1d_fwd / fcm_dw1d_step(dw1d_problem(...), x, w, bias, ...)   causal depthwise layer
     fcm_scan_fwd / fcm_scan_step(scan_problem(...), x, dt, A, Bm, Cm, ...)   selective scan
+    fcm_delta_fwd / fcm_delta_step(delta_problem(...), q, k, v, a, b, A, ...)   gated delta rule
     fcm_q4_fwd(q4_problem(...), x, q, scales, zeros, bias, y)   4-bit pointwise layer
+    fcm_mx4_quantize / fcm_mx4_dequantize / fcm_mx4_fwd / fcm_mx4x4_fwd(mx4_problem(...), ...)
+        microscaled 4-bit floating point
+    fcm_draft_verify(draft_problem(...), target, draft, tokens, ...)   drafted tokens
     fcm_beam_select / fcm_beam_reorder(beam_problem(...), ...)   beam search
 
 Tensor arguments are torch tensors on the GPU (or raw integer device addresses, or
@@ -119,6 +123,23 @@ class fcm_scan_problem(ctypes.Structure):
                [(n, _i64) for n in ("ldx", "lddt", "ldb", "ldc", "ldz", "ldy")]
 
 
+class fcm_delta_problem(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("dtype", "Hk", "Hv", "Dk", "Dv", "tokens", "seqs", "slots",
+                                    "qk_norm", "softplus")] + \
+               [(n, ctypes.c_float) for n in ("scale", "eps")] + \
+               [(n, _i64) for n in ("ldq", "ldk", "ldv", "lda", "ldb", "ldz", "ldy")]
+
+
+class fcm_mx4_problem(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("dtype", "M", "C", "K", "act")] + \
+               [(n, _i64) for n in ("ldx", "ldy")]
+
+
+class fcm_draft_problem(ctypes.Structure):
+    _fields_ = [(n, _i32) for n in ("dtype", "requests", "drafts", "vocab")] + \
+               [("temperature", ctypes.c_float)] + [(n, _i64) for n in ("ldt", "ldd")]
+
+
 class fcm_q4_problem(ctypes.Structure):
     _fields_ = [(n, _i32) for n in ("dtype", "M", "C", "K", "group", "act")] + \
                [(n, _i64) for n in ("ldx", "ldy")]
@@ -135,7 +156,9 @@ _POINTERS, _SIZES = ctypes.c_void_p * FCM_BEAM_POOLS, _i64 * FCM_BEAM_POOLS
 # every symbol include/fcm.h declares
 EXPORTS = ("fcm_dw1d_fwd", "fcm_dw1d_step", "fcm_scan_workspace", "fcm_scan_fwd",
            "fcm_scan_step", "fcm_q4_fwd", "fcm_beam_workspace", "fcm_beam_select",
-           "fcm_beam_reorder",
+           "fcm_beam_reorder", "fcm_delta_workspace", "fcm_delta_fwd", "fcm_delta_step",
+           "fcm_mx4_quantize", "fcm_mx4_dequantize", "fcm_mx4_fwd", "fcm_mx4x4_fwd",
+           "fcm_draft_workspace", "fcm_draft_verify",
            "fcm_default_device_spec", "fcm_query_device_spec", "fcm_plan", "fcm_plan_variant",
            "fcm_plan_chain",
            "fcm_num_variants", "fcm_variant_name", "fcm_pack_weights", "fcm_dwpw_fwd",
@@ -208,6 +231,17 @@ def lib() -> ctypes.CDLL:
             L.fcm_beam_select.argtypes = [P(fcm_beam_problem)] + [vp] * 9
             L.fcm_beam_reorder.argtypes = [P(fcm_beam_problem), vp, vp, vp, _i32, P(vp),
                                            P(_i64), P(_i64), vp]
+            L.fcm_delta_workspace.argtypes = [P(fcm_delta_problem)]
+            L.fcm_delta_workspace.restype = _i64
+            L.fcm_delta_fwd.argtypes = [P(fcm_delta_problem)] + [vp] * 16
+            L.fcm_delta_step.argtypes = [P(fcm_delta_problem)] + [vp] * 13
+            L.fcm_mx4_quantize.argtypes = [P(fcm_mx4_problem)] + [vp] * 4
+            L.fcm_mx4_dequantize.argtypes = [P(fcm_mx4_problem)] + [vp] * 4
+            L.fcm_mx4_fwd.argtypes = [P(fcm_mx4_problem)] + [vp] * 6
+            L.fcm_mx4x4_fwd.argtypes = [P(fcm_mx4_problem)] + [vp] * 7
+            L.fcm_draft_workspace.argtypes = [P(fcm_draft_problem)]
+            L.fcm_draft_workspace.restype = _i64
+            L.fcm_draft_verify.argtypes = [P(fcm_draft_problem)] + [vp] * 9
             L.fcm_status_str.restype = ctypes.c_char_p
             L.fcm_status_str.argtypes = [ctypes.c_int]
             L.fcm_last_error.restype = ctypes.c_char_p
@@ -218,7 +252,9 @@ def lib() -> ctypes.CDLL:
                          "fcm_pw_fwd", "fcm_conv_fwd", "fcm_pwdwpw_fwd", "fcm_pwdwpw_lbl",
                          "fcm_pwdwpw_lbl_noalloc", "fcm_tune_pwdwpw", "fcm_tune", "fcm_dw1d_fwd",
                          "fcm_dw1d_step", "fcm_scan_fwd", "fcm_scan_step", "fcm_q4_fwd",
-                         "fcm_beam_select", "fcm_beam_reorder"):
+                         "fcm_beam_select", "fcm_beam_reorder", "fcm_delta_fwd", "fcm_delta_step",
+                         "fcm_mx4_quantize", "fcm_mx4_dequantize", "fcm_mx4_fwd", "fcm_mx4x4_fwd",
+                         "fcm_draft_verify"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -497,6 +533,28 @@ def scan_problem(dtype="f16", D=8, N=16, groups=1, tokens=1, seqs=1, slots=0, so
                             int(bool(softplus)), ldx, lddt, ldb, ldc, ldz, ldy)
 
 
+def delta_problem(dtype="f16", Hk=1, Hv=1, Dk=8, Dv=8, tokens=1, seqs=1, slots=0, qk_norm=True,
+                  softplus=True, scale=0.0, eps=1e-6, ldq=0, ldk=0, ldv=0, lda=0, ldb=0, ldz=0,
+                  ldy=0) -> fcm_delta_problem:
+    """Gated delta rule of Hv value heads (Hk key heads, each shared by Hv/Hk of them) with states of
+    [Dk, Dv].  scale 0: 1/sqrt(Dk).  Row strides in elements; 0: dense."""
+    return fcm_delta_problem(_code(dtype), Hk, Hv, Dk, Dv, tokens, seqs, slots, int(bool(qk_norm)),
+                             int(bool(softplus)), scale, eps, ldq, ldk, ldv, lda, ldb, ldz, ldy)
+
+
+def mx4_problem(dtype="f16", M=1, C=32, K=1, act="none", ldx=0, ldy=0) -> fcm_mx4_problem:
+    """M rows of C channels in microscaled 4-bit blocks of 32, or a pointwise layer C -> K with such
+    weights for M tokens."""
+    return fcm_mx4_problem(_code(dtype), M, C, K, ACT_CODES[act] if isinstance(act, str) else act,
+                           ldx, ldy)
+
+
+def draft_problem(dtype="f32", requests=1, drafts=1, vocab=1, temperature=1.0, ldt=0,
+                  ldd=0) -> fcm_draft_problem:
+    """Verification of up to `drafts` drafted tokens of each request over `vocab` tokens."""
+    return fcm_draft_problem(_code(dtype), requests, drafts, vocab, temperature, ldt, ldd)
+
+
 def q4_problem(dtype="f16", M=1, C=8, K=8, group=128, act="none", ldx=0,
                ldy=0) -> fcm_q4_problem:
     """Pointwise layer C -> K with 4-bit weights, `group` channels to a scale, for M tokens."""
@@ -544,6 +602,62 @@ def fcm_scan_step(prob, x, dt, A, Bm, Cm, skip, dt_bias, z, slots, state, y, str
 def fcm_q4_fwd(prob, x, q, scales, zeros, bias, y, stream=None):
     _check(lib().fcm_q4_fwd(prob, _ptr(x), _ptr(q), _ptr(scales), _ptr(zeros), _ptr(bias),
                             _ptr(y), _stream(stream)), "fcm_q4_fwd")
+
+
+def _workspace(prob, name: str) -> int:
+    n = getattr(lib(), name)(prob)
+    if n < 0:
+        _check(FCM_ERR_INVALID_ARG, name)
+    return n
+
+
+def fcm_delta_workspace(prob) -> int:
+    return _workspace(prob, "fcm_delta_workspace")
+
+
+def fcm_delta_fwd(prob, q, k, v, a, b, A, dt_bias, norm, z, cu, slots, carry, state, workspace, y,
+                  stream=None):
+    _check(lib().fcm_delta_fwd(prob, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b), _ptr(A),
+                               _ptr(dt_bias), _ptr(norm), _ptr(z), _ptr(cu), _ptr(slots),
+                               _ptr(carry), _ptr(state), _ptr(workspace), _ptr(y),
+                               _stream(stream)), "fcm_delta_fwd")
+
+
+def fcm_delta_step(prob, q, k, v, a, b, A, dt_bias, norm, z, slots, state, y, stream=None):
+    _check(lib().fcm_delta_step(prob, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(b), _ptr(A),
+                                _ptr(dt_bias), _ptr(norm), _ptr(z), _ptr(slots), _ptr(state),
+                                _ptr(y), _stream(stream)), "fcm_delta_step")
+
+
+def fcm_mx4_quantize(prob, x, q, scales, stream=None):
+    _check(lib().fcm_mx4_quantize(prob, _ptr(x), _ptr(q), _ptr(scales), _stream(stream)),
+           "fcm_mx4_quantize")
+
+
+def fcm_mx4_dequantize(prob, q, scales, y, stream=None):
+    _check(lib().fcm_mx4_dequantize(prob, _ptr(q), _ptr(scales), _ptr(y), _stream(stream)),
+           "fcm_mx4_dequantize")
+
+
+def fcm_mx4_fwd(prob, x, q, scales, bias, y, stream=None):
+    _check(lib().fcm_mx4_fwd(prob, _ptr(x), _ptr(q), _ptr(scales), _ptr(bias), _ptr(y),
+                             _stream(stream)), "fcm_mx4_fwd")
+
+
+def fcm_mx4x4_fwd(prob, xq, xscales, q, scales, bias, y, stream=None):
+    _check(lib().fcm_mx4x4_fwd(prob, _ptr(xq), _ptr(xscales), _ptr(q), _ptr(scales), _ptr(bias),
+                               _ptr(y), _stream(stream)), "fcm_mx4x4_fwd")
+
+
+def fcm_draft_workspace(prob) -> int:
+    return _workspace(prob, "fcm_draft_workspace")
+
+
+def fcm_draft_verify(prob, target, draft, tokens, counts, uniform, workspace, accepted, next_token,
+                     stream=None):
+    _check(lib().fcm_draft_verify(prob, _ptr(target), _ptr(draft), _ptr(tokens), _ptr(counts),
+                                  _ptr(uniform), _ptr(workspace), _ptr(accepted), _ptr(next_token),
+                                  _stream(stream)), "fcm_draft_verify")
 
 
 def fcm_beam_workspace(prob) -> int:

@@ -40,8 +40,11 @@ SOURCES = [
     ("kernels/b2b.hip", True),
     ("kernels/dw1d.hip", True),
     ("kernels/scan.hip", True),
+    ("kernels/delta.hip", True),
     ("kernels/q4.hip", True),
+    ("kernels/mx4.hip", True),
     ("kernels/beam.hip", True),
+    ("kernels/draft.hip", True),
     ("api.cpp", True),
     ("api_seq.cpp", True),
     ("plan.cpp", False),

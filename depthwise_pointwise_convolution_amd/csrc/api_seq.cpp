@@ -1,7 +1,9 @@
 // api_seq.cpp -- the C ABI of the sequence operators: argument checks and dispatch.
 // Every check happens on the host before anything is enqueued.
 #include <hip/hip_runtime.h>
+#include <float.h>
 #include <limits.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -173,6 +175,114 @@ fcm_status scan_args(const fcm_scan_problem* p, const void* x, const void* dt, c
     return FCM_OK;
 }
 
+fcm_status check_delta(const fcm_delta_problem* p) {
+    if (!p) return invalid("problem is NULL");
+    SEQ_TRY(float_type(p->dtype));
+    if (p->Hk < 1 || p->Hv < 1 || p->Dk < 1 || p->Dv < 1 || p->tokens < 0 || p->seqs < 0 || p->slots < 0)
+        return invalid("Hk, Hv, Dk and Dv must be positive, tokens, seqs and slots not negative");
+    if (p->Hv % p->Hk != 0) return invalid("Hk must divide Hv");
+    if (p->Dk > 256 || p->Dv > 256) return unsupported("heads of more than 256 channels");
+    if (p->Hv > (1 << 16)) return unsupported("more than 2^16 heads");
+    if (p->qk_norm != 0 && p->qk_norm != 1) return invalid("qk_norm must be 0 or 1");
+    if (p->softplus != 0 && p->softplus != 1) return invalid("softplus must be 0 or 1");
+    if (!(p->eps > 0.0f) || !(p->eps <= FLT_MAX)) return invalid("eps must be above zero");
+    if (!(p->scale >= -FLT_MAX && p->scale <= FLT_MAX)) return invalid("scale must be finite");
+    if ((long long)p->tokens + p->seqs > (1 << 30)) return invalid("tokens + seqs is above 2^30");
+    if (delta_threads(*p) >= kThreads) return unsupported("too many tokens or sequences for one launch");
+    return FCM_OK;
+}
+
+fcm_status delta_args(const fcm_delta_problem* p, const void* q, const void* k, const void* v,
+                      const void* ga, const void* gb, const float* A, const float* dt_bias,
+                      const float* norm, const void* z, const int32_t* slots, float* state, void* y,
+                      DeltaArgs* a) {
+    const int e = elem(p->dtype);
+    NEED(A, 4);
+    if (p->tokens > 0) {
+        NEED(q, e);
+        NEED(k, e);
+        NEED(v, e);
+        SEQ_TRY(tensor(ga, e, "a is NULL", "a is misaligned for its type"));
+        SEQ_TRY(tensor(gb, e, "b is NULL", "b is misaligned for its type"));
+        NEED(y, e);
+    }
+    MAYBE(dt_bias, 4);
+    MAYBE(norm, 4);
+    MAYBE(z, e);
+    MAYBE(state, 4);
+    memset(a, 0, sizeof(*a));
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->a = ga;
+    a->b = gb;
+    a->A = A;
+    a->dt_bias = dt_bias;
+    a->norm = norm;
+    a->z = z;
+    a->slots = slots;
+    a->state = state;
+    a->y = y;
+    a->ldq = p->ldq;
+    a->ldk = p->ldk;
+    a->ldv = p->ldv;
+    a->lda = p->lda;
+    a->ldb = p->ldb;
+    a->ldz = p->ldz;
+    a->ldy = p->ldy;
+    SEQ_TRY(stride(&a->ldq, (long long)p->Hk * p->Dk));
+    SEQ_TRY(stride(&a->ldk, (long long)p->Hk * p->Dk));
+    SEQ_TRY(stride(&a->ldv, (long long)p->Hv * p->Dv));
+    SEQ_TRY(stride(&a->lda, p->Hv));
+    SEQ_TRY(stride(&a->ldb, p->Hv));
+    SEQ_TRY(stride(&a->ldz, (long long)p->Hv * p->Dv));
+    SEQ_TRY(stride(&a->ldy, (long long)p->Hv * p->Dv));
+    a->scale = p->scale != 0.0f ? p->scale : 1.0f / sqrtf((float)p->Dk);
+    a->eps = p->eps;
+    a->Hk = p->Hk;
+    a->Hv = p->Hv;
+    a->Dk = p->Dk;
+    a->Dv = p->Dv;
+    a->tokens = p->tokens;
+    a->seqs = p->seqs;
+    a->nslots = p->slots;
+    a->qk_norm = p->qk_norm;
+    a->softplus = p->softplus;
+    return FCM_OK;
+}
+
+fcm_status check_mx4(const fcm_mx4_problem* p, bool product) {
+    if (!p) return invalid("problem is NULL");
+    SEQ_TRY(float_type(p->dtype));
+    if (p->M < 0 || p->C < 1 || (product && p->K < 1))
+        return invalid("C and K must be positive, M not negative");
+    if (p->C % 32 != 0) return unsupported("C must be a multiple of 32");
+    if (p->C > (1 << 20)) return unsupported("C above 2^20");
+    if (!product) {
+        if ((long long)p->M * p->C > (1ll << 36)) return unsupported("M * C above 2^36");
+        return FCM_OK;
+    }
+    if (p->dtype == FCM_F32) return unsupported("4-bit weights need 16-bit activations");
+    if (p->act < FCM_ACT_NONE || p->act > FCM_ACT_RELU6) return invalid("act is not an fcm_act");
+    if (p->M > (1 << 20) || p->K > (1 << 24)) return unsupported("M above 2^20, K above 2^24");
+    return FCM_OK;
+}
+
+fcm_status check_draft(const fcm_draft_problem* p) {
+    if (!p) return invalid("problem is NULL");
+    SEQ_TRY(float_type(p->dtype));
+    if (p->requests < 0 || p->drafts < 1 || p->vocab < 1)
+        return invalid("drafts and vocab must be positive, requests not negative");
+    if (p->drafts > 64) return unsupported("more than 64 drafted tokens of a request");
+    if (p->vocab > INT_MAX - (1 << 25) + 1) return unsupported("vocab above 2^31 - 2^25");
+    if (!(p->temperature >= 0.0f && p->temperature <= FLT_MAX))
+        return invalid("temperature must be zero or above, and finite");
+    if (p->requests > (1 << 24)) return unsupported("requests above 2^24");
+    if (draft_threads(*p) >= kThreads)
+        return unsupported("too large requests * drafts * vocab for one launch");
+    return FCM_OK;
+}
+
 fcm_status check_beam(const fcm_beam_problem* p) {
     if (!p) return invalid("problem is NULL");
     SEQ_TRY(float_type(p->dtype));
@@ -299,6 +409,181 @@ fcm_status fcm_q4_fwd(const fcm_q4_problem* prob, const void* x, const void* q,
     a.group = p.group;
     a.act = p.act;
     return done(launch_q4(a, p.dtype, stream));
+}
+
+int64_t fcm_delta_workspace(const fcm_delta_problem* prob) {
+    if (check_delta(prob) != FCM_OK) return -1;
+    set_error(FCM_OK, nullptr);
+    return delta_workspace_bytes(*prob);
+}
+
+fcm_status fcm_delta_fwd(const fcm_delta_problem* prob, const void* q, const void* k, const void* v,
+                         const void* a, const void* b, const float* A, const float* dt_bias,
+                         const float* norm, const void* z, const int32_t* cu, const int32_t* slots,
+                         const int32_t* carry, float* state, void* workspace, void* y, void* stream) {
+    SEQ_TRY(check_delta(prob));
+    SEQ_TRY(sequences(prob->tokens, prob->seqs, prob->slots, cu, slots, carry, state));
+    DeltaArgs args;
+    SEQ_TRY(delta_args(prob, q, k, v, a, b, A, dt_bias, norm, z, slots, state, y, &args));
+    NEED(workspace, 16);
+    args.cu = cu;
+    args.carry = carry;
+    args.ws = workspace;
+    if (prob->seqs == 0) return done(0);
+    return done(launch_delta_fwd(args, prob->dtype, stream));
+}
+
+fcm_status fcm_delta_step(const fcm_delta_problem* prob, const void* q, const void* k, const void* v,
+                          const void* a, const void* b, const float* A, const float* dt_bias,
+                          const float* norm, const void* z, const int32_t* slots, float* state, void* y,
+                          void* stream) {
+    SEQ_TRY(check_delta(prob));
+    if (prob->tokens != prob->seqs) return invalid("the single-token call needs tokens == seqs");
+    NEED(state, 4);
+    MAYBE(slots, 4);
+    if (!slots && prob->slots < prob->seqs) return invalid("slots == NULL needs at least seqs slots");
+    DeltaArgs args;
+    SEQ_TRY(delta_args(prob, q, k, v, a, b, A, dt_bias, norm, z, slots, state, y, &args));
+    if (prob->seqs == 0) return done(0);
+    return done(launch_delta_step(args, prob->dtype, stream));
+}
+
+fcm_status fcm_mx4_quantize(const fcm_mx4_problem* prob, const void* x, void* q, uint8_t* scales,
+                            void* stream) {
+    SEQ_TRY(check_mx4(prob, false));
+    Mx4Args a;
+    memset(&a, 0, sizeof(a));
+    a.ldx = prob->ldx;
+    SEQ_TRY(stride(&a.ldx, prob->C));
+    if (prob->M == 0) return done(0);
+    NEED(x, elem(prob->dtype));
+    NEED(q, 16);
+    NEED(scales, 1);
+    a.x = x;
+    a.q = (const uint8_t*)q;
+    a.scales = scales;
+    a.M = prob->M;
+    a.C = prob->C;
+    return done(launch_mx4_quantize(a, prob->dtype, stream));
+}
+
+fcm_status fcm_mx4_dequantize(const fcm_mx4_problem* prob, const void* q, const uint8_t* scales,
+                              void* y, void* stream) {
+    SEQ_TRY(check_mx4(prob, false));
+    Mx4Args a;
+    memset(&a, 0, sizeof(a));
+    a.ldy = prob->ldy;
+    SEQ_TRY(stride(&a.ldy, prob->C));
+    if (prob->M == 0) return done(0);
+    NEED(q, 16);
+    NEED(scales, 1);
+    NEED(y, elem(prob->dtype));
+    a.q = (const uint8_t*)q;
+    a.scales = scales;
+    a.y = y;
+    a.M = prob->M;
+    a.C = prob->C;
+    return done(launch_mx4_dequantize(a, prob->dtype, stream));
+}
+
+fcm_status fcm_mx4_fwd(const fcm_mx4_problem* prob, const void* x, const void* q, const uint8_t* scales,
+                       const float* bias, void* y, void* stream) {
+    SEQ_TRY(check_mx4(prob, true));
+    Mx4Args a;
+    memset(&a, 0, sizeof(a));
+    a.ldx = prob->ldx;
+    a.ldy = prob->ldy;
+    SEQ_TRY(stride(&a.ldx, prob->C));
+    SEQ_TRY(stride(&a.ldy, prob->K));
+    if (a.ldx % 8 != 0) return invalid("ldx must be a multiple of 8");
+    if (a.ldx >= (1ll << 26)) return unsupported("ldx of 2^26 or more");
+    NEED(q, 16);
+    NEED(scales, 1);
+    MAYBE(bias, 4);
+    if (prob->M == 0) return done(0);
+    NEED(x, 16);
+    NEED(y, 2);
+    a.x = x;
+    a.q = (const uint8_t*)q;
+    a.scales = scales;
+    a.bias = bias;
+    a.y = y;
+    a.M = prob->M;
+    a.C = prob->C;
+    a.K = prob->K;
+    a.act = prob->act;
+    return done(launch_mx4(a, prob->dtype, stream));
+}
+
+fcm_status fcm_mx4x4_fwd(const fcm_mx4_problem* prob, const void* xq, const uint8_t* xscales,
+                         const void* q, const uint8_t* scales, const float* bias, void* y,
+                         void* stream) {
+    SEQ_TRY(check_mx4(prob, true));
+    if (mx4x4_threads(*prob) >= kThreads) return unsupported("too large M * K for one launch");
+    Mx4Args a;
+    memset(&a, 0, sizeof(a));
+    a.ldy = prob->ldy;
+    SEQ_TRY(stride(&a.ldy, prob->K));
+    NEED(q, 16);
+    NEED(scales, 1);
+    MAYBE(bias, 4);
+    if (prob->M == 0) return done(0);
+    NEED(xq, 16);
+    NEED(xscales, 1);
+    NEED(y, 2);
+    a.x = xq;
+    a.xscales = xscales;
+    a.q = (const uint8_t*)q;
+    a.scales = scales;
+    a.bias = bias;
+    a.y = y;
+    a.M = prob->M;
+    a.C = prob->C;
+    a.K = prob->K;
+    a.act = prob->act;
+    return done(launch_mx4x4(a, prob->dtype, stream));
+}
+
+int64_t fcm_draft_workspace(const fcm_draft_problem* prob) {
+    if (check_draft(prob) != FCM_OK) return -1;
+    set_error(FCM_OK, nullptr);
+    return draft_workspace_bytes(*prob);
+}
+
+fcm_status fcm_draft_verify(const fcm_draft_problem* prob, const void* target, const void* draft,
+                            const int32_t* tokens, const int32_t* counts, const float* uniform,
+                            void* workspace, int32_t* accepted, int32_t* next, void* stream) {
+    SEQ_TRY(check_draft(prob));
+    const int e = elem(prob->dtype);
+    DraftArgs a;
+    memset(&a, 0, sizeof(a));
+    a.ldt = prob->ldt;
+    a.ldd = prob->ldd;
+    SEQ_TRY(stride(&a.ldt, prob->vocab));
+    SEQ_TRY(stride(&a.ldd, prob->vocab));
+    if (prob->requests == 0) return done(0);
+    NEED(target, e);
+    MAYBE(draft, e);
+    NEED(tokens, 4);
+    MAYBE(counts, 4);
+    if (prob->temperature > 0.0f) NEED(uniform, 4);
+    MAYBE(uniform, 4);
+    NEED(workspace, 16);
+    NEED(accepted, 4);
+    NEED(next, 4);
+    a.target = target;
+    a.draft = draft;
+    a.tokens = tokens;
+    a.counts = counts;
+    a.uniform = uniform;
+    a.ws = workspace;
+    a.accepted = accepted;
+    a.next = next;
+    a.temperature = prob->temperature;
+    a.requests = prob->requests;
+    a.drafts = prob->drafts;
+    a.vocab = prob->vocab;
+    return done(launch_draft_verify(a, prob->dtype, stream));
 }
 
 int64_t fcm_beam_workspace(const fcm_beam_problem* prob) {

@@ -492,6 +492,48 @@ fcm_status fcm_scan_step(const fcm_scan_problem* prob, const void* x, const void
                          const float* dt_bias, const void* z, const int32_t* slots,
                          float* state, void* y, void* stream);
 
+/* Gated delta rule.  Value head h of Hv has the queries and keys of head h / (Hv/Hk) of Hk, and a
+ * state S, [Dk][Dv]:
+ *   q' = scale * q, k' = k, each divided by sqrt(sum of its squares + eps) if `qk_norm`
+ *   alpha = exp(A[h] * d), d = a[t][h] + dt_bias[h], through softplus if `softplus`
+ *   beta = 1 / (1 + exp(-b[t][h]))
+ *   S <- alpha * S;  S[i][j] <- S[i][j] + beta * k'[i] * (v[j] - sum_c k'[c] * S[c][j])
+ *   o[j] = sum_i q'[i] * S[i][j]
+ *   y[t][h][j] = o[j] * (norm ? norm[j] / sqrt(mean of o's squares + eps) : 1) * (z ? z * sigmoid(z) : 1)
+ * A <= 0 and beta * |k'|^2 < 2 keep the recurrence bounded.  A step d of zero keeps the state, whatever
+ * A.  Prompts are computed in chunks of 64 tokens: a value that is not finite makes the outputs of its
+ * own head's whole chunk, and the head's outputs and state after it, possibly not finite; other heads and
+ * sequences are as they would be without it. */
+typedef struct {
+    int32_t dtype;    /* FCM_F32, FCM_F16 or FCM_BF16: q, k, v, a, b, z, y */
+    int32_t Hk, Hv;   /* key heads; value heads, a multiple of Hk */
+    int32_t Dk, Dv;   /* a head's channels, 1 to 256 */
+    int32_t tokens, seqs, slots; /* as for the depthwise layer */
+    int32_t qk_norm;  /* 1: queries and keys are normalised */
+    int32_t softplus; /* 1: d goes through softplus */
+    float scale;      /* of the queries; 0: 1 / sqrt(Dk) */
+    float eps;        /* above zero */
+    int64_t ldq, ldk, ldv, lda, ldb, ldz, ldy;
+} fcm_delta_problem;
+
+/* Bytes of device memory fcm_delta_fwd needs, or -1 as for fcm_scan_workspace. */
+int64_t fcm_delta_workspace(const fcm_delta_problem* prob);
+
+/* Prompts.  q, k: [tokens][Hk][Dk]; v, z, y: [tokens][Hv][Dv] (z may be NULL); a, b: [tokens][Hv];
+ * A: [Hv] fp32; dt_bias: [Hv] fp32 or NULL; norm: [Dv] fp32 or NULL; state: [slots][Hv][Dk][Dv] fp32,
+ * read where carry says so and always written (NULL as for fcm_dw1d_fwd); workspace as for
+ * fcm_scan_fwd.  With a norm, o is rounded to the storage type once before it (its squares are not). */
+fcm_status fcm_delta_fwd(const fcm_delta_problem* prob, const void* q, const void* k, const void* v,
+                         const void* a, const void* b, const float* A, const float* dt_bias,
+                         const float* norm, const void* z, const int32_t* cu, const int32_t* slots,
+                         const int32_t* carry, float* state, void* workspace, void* y, void* stream);
+
+/* One token of each sequence: the state in slots[b] is read and updated in place. */
+fcm_status fcm_delta_step(const fcm_delta_problem* prob, const void* q, const void* k, const void* v,
+                          const void* a, const void* b, const float* A, const float* dt_bias,
+                          const float* norm, const void* z, const int32_t* slots, float* state, void* y,
+                          void* stream);
+
 /* Pointwise layer with 4-bit weights for a few tokens:
  *   y[m][k] = act(bias[k] + sum_c (q[k][c] - zeros[k][c/group]) * scales[k][c/group] * x[m][c])
  * q: [K][C/2], two codes of 0..15 a byte, the even channel in the low half; scales:
@@ -513,6 +555,75 @@ typedef struct {
 fcm_status fcm_q4_fwd(const fcm_q4_problem* prob, const void* x, const void* q,
                       const void* scales, const uint8_t* zeros, const float* bias, void* y,
                       void* stream);
+
+/* Microscaled 4-bit floating point: rows of C channels in blocks of 32.  A channel's code is a sign
+ * bit, two bits of exponent and one of mantissa (0, 0.5, 1, 1.5, 2, 3, 4 or 6), the even channel in
+ * the low half of a byte: [rows][C/2] uint8.  A block's scale is a power of two, kept as its exponent
+ * plus 127: [rows][C/32] uint8; 255 makes the whole block NaN.  Both arrays are dense. */
+typedef struct {
+    int32_t dtype;   /* quantisation: FCM_F32, FCM_F16 or FCM_BF16; products: FCM_F16 or FCM_BF16 */
+    int32_t M, C, K; /* rows; channels, a multiple of 32; output channels (of products) */
+    int32_t act;     /* fcm_act (of products) */
+    int64_t ldx, ldy;
+} fcm_mx4_problem;
+
+/* Codes q and scales of x, [M][C] (row stride ldx): a block's exponent is that of its largest
+ * magnitude less 2, not below -127; values are rounded to the nearest code, ties to the even one, and
+ * end at 6.  A block of zeros has the scale 2^-127; one with an infinity or NaN has 255.  q needs 16-byte
+ * alignment. */
+fcm_status fcm_mx4_quantize(const fcm_mx4_problem* prob, const void* x, void* q, uint8_t* scales,
+                            void* stream);
+
+/* The values that codes and scales stand for, rounded to y's type: y [M][C] (row stride ldy). */
+fcm_status fcm_mx4_dequantize(const fcm_mx4_problem* prob, const void* q, const uint8_t* scales,
+                              void* y, void* stream);
+
+/* Pointwise layer y[m][k] = act(bias[k] + sum_c W[k][c] * x[m][c]) with W in codes: q [K][C/2], scales
+ * [K][C/32], bias [K] fp32 or NULL.  x: [M][C] in the storage type; for a few tokens (the weights are
+ * read once for every 32 of them).  Products of a block's values are exact and summed in fp32.  x and q need
+ * 16-byte alignment and ldx a multiple of 8. */
+fcm_status fcm_mx4_fwd(const fcm_mx4_problem* prob, const void* x, const void* q, const uint8_t* scales,
+                       const float* bias, void* y, void* stream);
+
+/* The same with x in codes too, xq [M][C/2] and xscales [M][C/32], on the scaled matrix instructions,
+ * for any number of tokens.  xq and q need 16-byte alignment; ldx is not used. */
+fcm_status fcm_mx4x4_fwd(const fcm_mx4_problem* prob, const void* xq, const uint8_t* xscales,
+                         const void* q, const uint8_t* scales, const float* bias, void* y,
+                         void* stream);
+
+/* Verification of drafted tokens: how many of a request's drafted tokens stand, and the token that
+ * follows them. */
+typedef struct {
+    int32_t dtype;     /* FCM_F32, FCM_F16 or FCM_BF16: logits */
+    int32_t requests;
+    int32_t drafts;    /* places for drafted tokens of a request, 1 to 64 */
+    int32_t vocab;     /* up to 2^31 - 2^25 */
+    float temperature; /* logits are divided by it; 0: the largest logit alone counts */
+    int64_t ldt, ldd;  /* row strides of the target's and the draft's logits */
+} fcm_draft_problem;
+
+/* Bytes of device memory fcm_draft_verify needs, or -1 as for fcm_scan_workspace. */
+int64_t fcm_draft_workspace(const fcm_draft_problem* prob);
+
+/* With p_i the target's probabilities in place i (softmax of its logits / temperature; row i of a
+ * request's drafts+1) and q_i the draft's that token x_i was drawn from, x_0, x_1, .. stand as long as
+ *   uniform[i] * q_i(x_i) < p_i(x_i).
+ * The token after them is drawn, with r = uniform[drafts], from max(p_i - q_i, 0) in the place i of the first
+ * that does not stand, or from p_i behind the last: the lowest token whose weight, with those of the tokens
+ * below it, is above r times that of all.  Where the draft never differs (all weights are zero), p_i itself is
+ * drawn from.  With temperature 0 a token stands if it has the largest logit (the lowest of equal ones), and the
+ * token after is that one.  draft NULL: a drafted token had probability 1.
+ * -inf logits are masked tokens; NaN counts as -inf and +inf as the largest float.  In a target's row without
+ * any finite logit no token stands, and the token after is -1; such a row of the draft has no weights, so a token with any
+ * target probability stands.  A drafted token outside the vocabulary does not stand.
+ * target: [requests*(drafts+1)][vocab]; draft: [requests*drafts][vocab] or NULL; tokens:
+ * [requests*drafts] int32; counts: [requests] int32 or NULL (drafts), how many of its tokens a request uses
+ * (clamped to 0 .. drafts; the rest of its rows is not looked at); uniform:
+ * [requests*(drafts+1)] fp32 in [0, 1) (not read with temperature 0, where it may be NULL).  Out: accepted and next,
+ * [requests] int32.  workspace: 16-byte aligned. */
+fcm_status fcm_draft_verify(const fcm_draft_problem* prob, const void* target, const void* draft,
+                            const int32_t* tokens, const int32_t* counts, const float* uniform,
+                            void* workspace, int32_t* accepted, int32_t* next, void* stream);
 
 /* Beam search: the next beams of each request, and the states that go with them. */
 typedef struct {
