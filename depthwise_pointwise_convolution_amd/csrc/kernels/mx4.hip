@@ -306,57 +306,455 @@ int pick_tokens(const Mx4Args& a, hipStream_t s) {
 // ------------------------------------------------------------------------------------------
 // tokens in 4 bits too
 // ------------------------------------------------------------------------------------------
-// A workgroup of four waves has 128 x 128 outputs, a wave 64 x 64.
-template <typename T>
-__global__ __launch_bounds__(256) void mx4x4_kernel(Mx4Args a, int ktiles) {
-    const int lane = threadIdx.x & 63, sub = lane & 15, grp = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m0 = blockIdx.x / ktiles * 128 + (wave >> 1) * 64, k0 = blockIdx.x % ktiles * 128 + (wave & 1) * 64;
-    const int blocks = a.C / 32;
-    const uint8_t* x = (const uint8_t*)a.x;
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
-    for (int b = 0; b < blocks; b += 4) {
-        i32x8 fx[4], fw[4];
-        int sx[4], sw[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // (rows behind the last repeat it, and are not stored)
-            const int m = m0 + 16 * i + sub < a.M ? m0 + 16 * i + sub : a.M - 1;
-            const int k = k0 + 16 * i + sub < a.K ? k0 + 16 * i + sub : a.K - 1;
-            u32x4 vx = {}, vw = {};
-            sx[i] = sw[i] = 0;
-            if (b + grp < blocks) {
-                vx = ld16(x + ((long long)m * blocks + b + grp) * 16);
-                vw = ld16(a.q + ((long long)k * blocks + b + grp) * 16);
-                sx[i] = a.xscales[(long long)m * blocks + b + grp];
-                sw[i] = a.scales[(long long)k * blocks + b + grp];
-            }
-            fx[i] = i32x8{(int)vx[0], (int)vx[1], (int)vx[2], (int)vx[3], 0, 0, 0, 0};
-            fw[i] = i32x8{(int)vw[0], (int)vw[1], (int)vw[2], (int)vw[3], 0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fx[i], fw[j], acc[i][j], 4, 4, 0, sx[i], 0, sw[j]);
-    }
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+
+__device__ __forceinline__ i32x8 fp4_operand(u32x4 v) {
+    return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+}
+
+// The bias of a tile's output channels k0 .. in LDS, once all waves are done with what was there.
+__device__ __forceinline__ void stage_bias(const Mx4Args& a, float* to, int n, int k0) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = a.bias && k0 + i < a.K ? a.bias[k0 + i] : 0.0f;
+    __syncthreads();
+}
+
+// A wave's RK x RM accumulators, of output channels k0 .. and tokens m0 .., through its own LDS, a tile of tokens at a
+// time.  Row e of a lane's accumulator is output channel 8 * (e / 4) + 4 * half + e % 4, of token `sub`.
+template <typename T, int RK, int RM>
+__device__ __forceinline__ void store_tiles(const Mx4Args& a, const f32x16 (&acc)[RK][RM], T* out, const float* bias, int m0, int k0) {
+    constexpr int PW = 32 * RK + 8;  // elements of a token in LDS
+    const int lane = threadIdx.x & 63, sub = lane & 31, half = lane >> 5;
     const Act act = act_bounds(a.act);
+    const bool whole = a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0 && m0 + 32 * RM <= a.M && k0 + 32 * RK <= a.K;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int k = k0 + 16 * j + sub;
+    for (int j = 0; j < RM; ++j) {
+#pragma unroll
+        for (int i = 0; i < RK; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int c = 32 * i + 8 * (e / 4) + 4 * half;
+                const f32x4 b = *(const f32x4*)(bias + c);
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = clamp_act(acc[i][j][e + q] + b[q], act);
+                *(uint2*)(out + sub * PW + c) = pack8<T>(v);
+            }
+        __builtin_amdgcn_wave_barrier();
+        constexpr int CH = 4 * RK, N = 32 * CH / 64;  // 16-byte pieces of a token, and of a lane
+        const int t = lane / CH, c = lane % CH * 8;
+        u32x4 v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = ld16(out + (t + 64 / CH * i) * PW + c);
+        T* y = (T*)a.y + (long long)(m0 + 32 * j + t) * a.ldy + k0 + c;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) st16(y + 64 / CH * i * a.ldy, v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const vec_t<T, 8> w = __builtin_bit_cast(vec_t<T, 8>, v[i]);
+                if (m0 + 32 * j + t + 64 / CH * i < a.M)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (k0 + c + q < a.K) y[64 / CH * i * a.ldy + q] = w[q];
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+constexpr int kSpan = 8;  // steps whose scales are loaded at a time: 32 bytes of a row
+
+// Workgroups of WK x WM waves; a wave has RK x RM tiles of 32 output channels x 32 tokens.  A step's 64 bytes of
+// every row are in registers while the one before is multiplied, then go to the other of two LDS buffers, in
+// 16-byte blocks whose place is turned by the row so that a column of them has no bank twice.
+//
+// A 32 x 32 x 64 product takes a block of each half of the wave, and any two blocks will do as long as both sides
+// take the same: in product j half g has block 2 g + j.  Output channels are the rows of the product: a lane has four
+// neighbouring ones of a token, which pass through LDS and are stored as 16 bytes.
+template <typename T, int WK, int WM, int RK, int RM>
+__global__ __launch_bounds__(64 * WK * WM, 2) void mx4x4_kernel(Mx4Args a, int mtiles, int ktiles) {
+    constexpr int NW = WK * WM, TK = 32 * WK * RK, TM = 32 * WM * RM, ROWS = TK + TM;
+    constexpr int KL = TK / (16 * NW), LOADS = ROWS / (16 * NW);  // of a thread: 16 rows for each wave
+    constexpr int SROWS = 16 * NW;                                // rows whose scales a step loads
+    static_assert(TK % SROWS == 0 && TM % SROWS == 0 && ROWS / SROWS <= kSpan, "a step's rows are of one side");
+    __shared__ u32x4 data[2][ROWS][4];
+    __shared__ u32x2 scale[2][kSpan / 2][ROWS];  // of two steps each
+    const int tid = threadIdx.x, lane = tid & 63, sub = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wk = wave % WK * (32 * RK), wm = wave / WK * (32 * RM);
+    // tiles in columns of 8 token tiles, an XCD's next to each other: they share rows in its L2
+    const int id = xcd_logical_id(blockIdx.x, gridDim.x);
+    const int band = id / (8 * ktiles), height = mtiles - 8 * band < 8 ? mtiles - 8 * band : 8;
+    const int m0 = (8 * band + id % (8 * ktiles) % height) * TM, k0 = id % (8 * ktiles) / height * TK;
+    const int blocks = a.C / 32, steps = (blocks + 3) / 4;
+    const int krows = a.K - k0 < TK ? a.K - k0 : TK, mrows = a.M - m0 < TM ? a.M - m0 : TM;
+    const uint32_t pitch = a.C / 2;
+    // (rows behind the last read as zero; a tile's rows are below 2^28 bytes)
+    const __amdgpu_buffer_rsrc_t rq = mm::rsrc(a.q + (long long)k0 * pitch, krows * pitch);
+    const __amdgpu_buffer_rsrc_t rx = mm::rsrc((const uint8_t*)a.x + (long long)m0 * pitch, mrows * pitch);
+    const int lrow = tid >> 2, chunk = tid & 3;
+    const uint32_t lat = lrow * pitch + 16 * chunk;
+    u32x4 raw[LOADS];
+    auto fetch = [&](int s) {
+        const bool in = 4 * s + chunk < blocks;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const bool tok = i >= KL;
+            const int r = 16 * NW * (tok ? i - KL : i);
+            raw[i] = __builtin_amdgcn_raw_buffer_load_b128(tok ? rx : rq, in && lrow + r < (tok ? mrows : krows) ? lat : mm::kOob,
+                                                           s * (kStep / 2) + r * pitch, 0);
+        }
+    };
+    auto stage = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) data[buf][lrow + 16 * NW * i][chunk ^ (lrow >> 2 & 3)] = raw[i];
+    };
+    // Scales of kSpan steps at a time: a step loads some of the rows, 32 bytes of four lanes each, for the steps after the
+    // present eight.  Where two steps have fewer than eight they are the last eight of the row, moved down on
+    // their way to LDS.  (A row behind the last takes the last one's: its outputs are not stored.  Rows of fewer than
+    // eight are loaded before the first step, and here any eight bytes, which no step uses.)
+    constexpr int PARTS = ROWS / SROWS;
+    u32x2 sraw;
+    const int spart = tid & 3;
+    const bool some = blocks >= 8;
+    const uint8_t* kscales = some ? a.scales + (long long)k0 * blocks : a.q;
+    const uint8_t* mscales = some ? a.xscales + (long long)m0 * blocks : a.q;
+    auto scale_at = [&](int group) {
+        const int b = 4 * kSpan * group + 8 * spart;
+        return b < blocks ? b : blocks & ~7;
+    };
+    auto fetch_scales = [&](int group, int part) {
+        const int want = scale_at(group), at = want + 8 <= blocks ? want : some ? blocks - 8 : 0;
+        const bool tok = SROWS * part >= TK;
+        const int r = SROWS * part + (tid >> 2) - (tok ? TK : 0), most = (tok ? mrows : krows) - 1;
+        return *(const u32x2_any*)((tok ? mscales : kscales) + (uint32_t)(r < most ? r : most) * (uint32_t)blocks + at);
+    };
+    auto stage_scales = [&](int group, int part, u32x2 v) {
+        const int want = scale_at(group), gone = want + 8 <= blocks ? 0 : want - (blocks - 8);  // (8: none left)
+        const uint64_t u = (__builtin_bit_cast(uint64_t, v) >> (4 * gone)) >> (4 * gone);
+        scale[group & 1][spart][SROWS * part + (tid >> 2)] = __builtin_bit_cast(u32x2, u);
+    };
+    f32x16 acc[RK][RM];
+#pragma unroll
+    for (int i = 0; i < RK; ++i)
+#pragma unroll
+        for (int j = 0; j < RM; ++j) acc[i][j] = f32x16{};
+    fetch(0);
+    if (some) {
+        u32x2 v[PARTS];
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) v[q] = fetch_scales(0, q);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) stage_scales(0, q, v[q]);
+    } else {
+        for (int row = tid; row < ROWS; row += 64 * NW) {
+            const bool tok = row >= TK;
+            const int r = tok ? row - TK : row, most = (tok ? mrows : krows) - 1;
+            const uint8_t* p = (tok ? a.xscales + (long long)m0 * blocks : a.scales + (long long)k0 * blocks) + (r < most ? r : most) * blocks;
+            u32x2 v = {0, 0};
+            for (int b = 0; b < blocks; ++b) v[b >> 2] |= (uint32_t)p[b] << (8 * (b & 3));
+            scale[0][0][row] = v;
+        }
+    }
+    stage(0);
+    fetch(steps > 1 ? 1 : 0);
+    sraw = fetch_scales(1, 0);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        // (without branches, which would pull loads and products apart: the last steps load and store once more, and
+        // the last parts' scales of a group are loaded again)
+        const int buf = s & 1;
+        auto part_of = [](int t) { return t % kSpan < PARTS ? t % kSpan : PARTS - 1; };
+        stage(buf ^ 1);
+        stage_scales(s / kSpan + 1, part_of(s), sraw);
+        fetch(s + 2 < steps ? s + 2 : steps - 1);
+        sraw = fetch_scales((s + 1) / kSpan + 1, part_of(s + 1));
+        // (the compiler would move the loads behind the products, where their registers are free sooner)
+        __builtin_amdgcn_sched_barrier(0);
+        const u32x2* sp = scale[s / kSpan & 1][s % kSpan / 2];
+        int sk[RK], sm[RM];
+#pragma unroll
+        for (int i = 0; i < RK; ++i) sk[i] = sp[wk + 32 * i + sub][s & 1] >> (16 * half);
+#pragma unroll
+        for (int i = 0; i < RM; ++i) sm[i] = sp[TK + wm + 32 * i + sub][s & 1] >> (16 * half);
+        auto block = [&](auto which) {
+            constexpr int J = decltype(which)::value;
+            i32x8 fk[RK], fm[RM];
+            const int place = (2 * half + J) ^ (sub >> 2 & 3);
+#pragma unroll
+            for (int i = 0; i < RK; ++i) fk[i] = fp4_operand(data[buf][wk + 32 * i + sub][place]);
+#pragma unroll
+            for (int i = 0; i < RM; ++i) fm[i] = fp4_operand(data[buf][TK + wm + 32 * i + sub][place]);
+#pragma unroll
+            for (int i = 0; i < RK; ++i)
+#pragma unroll
+                for (int j = 0; j < RM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fk[i], fm[j], acc[i][j], 4, 4, J, sk[i], J, sm[j]);
+        };
+        block(std::integral_constant<int, 0>());
+        block(std::integral_constant<int, 1>());
+        __syncthreads();
+    }
+    float* bias = (float*)&scale[0][0][0];
+    stage_bias(a, bias, TK, k0);
+    store_tiles<T, RK, RM>(a, acc, (T*)&data[0][0][0] + wave * 32 * (32 * RK + 8), bias + wk, m0 + wm, k0 + wk);
+    static_assert(NW * 32 * (32 * RK + 8) * (int)sizeof(T) <= (int)sizeof(data), "the outputs' LDS");
+}
+
+// The order of a block of 16 products: one of the first kind behind each of the first eight, one of the second behind the
+// others.
+constexpr int kProduct = 0x008, kLoad = 0x020, kLdsRead = 0x100, kLdsWrite = 0x200;
+template <int FIRST, int SECOND>
+__device__ __forceinline__ void order() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+        if (i < 8)
+            __builtin_amdgcn_sched_group_barrier(FIRST, 1, 0);
+        else
+            __builtin_amdgcn_sched_group_barrier(SECOND, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The same for products that fill the card: 256 x 256 outputs by four waves, 128 x 128 each in half of a SIMD's
+// registers, steps of 256 channels.  A wave reads operands at half the rate per product, so LDS no longer takes
+// longer than the matrix units; but there is one wave a SIMD, so its own instructions have to follow each other without a
+// pause.  A step is four blocks of 16 products; in each the next block's operands are read, and in turn the next
+// step goes to LDS and the one after is loaded.  The barrier between the third and the fourth says that all waves have
+// read this step and stored the next, whose first operands are read in the fourth.
+template <typename T>
+__global__ __launch_bounds__(256, 1) void mx4x4_large_kernel(Mx4Args a, int mtiles, int ktiles) {
+    constexpr int TILE = 256, ROWS = 2 * TILE, R = 4, LOADS = 16, SPAN = 4;
+    __shared__ u32x4 data[2][ROWS][8];
+    __shared__ u32x2 scale[2][SPAN][ROWS];
+    const int tid = threadIdx.x, lane = tid & 63, sub = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wk = wave % 2 * 128, wm = wave / 2 * 128;
+    const int id = xcd_logical_id(blockIdx.x, gridDim.x);
+    const int band = id / (8 * ktiles), height = mtiles - 8 * band < 8 ? mtiles - 8 * band : 8;
+    const int m0 = (8 * band + id % (8 * ktiles) % height) * TILE, k0 = id % (8 * ktiles) / height * TILE;
+    const int blocks = a.C / 32, steps = (blocks + 7) / 8;
+    const int krows = a.K - k0 < TILE ? a.K - k0 : TILE, mrows = a.M - m0 < TILE ? a.M - m0 : TILE;
+    const uint32_t pitch = a.C / 2;
+    const __amdgpu_buffer_rsrc_t rq = mm::rsrc(a.q + (long long)k0 * pitch, krows * pitch);
+    const __amdgpu_buffer_rsrc_t rx = mm::rsrc((const uint8_t*)a.x + (long long)m0 * pitch, mrows * pitch);
+    const int lrow = tid >> 3, chunk = tid & 7;
+    const uint32_t lat = lrow * pitch + 16 * chunk;
+    u32x4 raw[LOADS];
+    auto fetch = [&](int s, auto from) {  // eight of them
+        constexpr int F = decltype(from)::value;
+        const bool in = 8 * s + chunk < blocks;
+#pragma unroll
+        for (int i = F; i < F + 8; ++i) {
+            const int r = 32 * (i - F);
+            raw[i] = __builtin_amdgcn_raw_buffer_load_b128(F ? rx : rq, in && lrow + r < (F ? mrows : krows) ? lat : mm::kOob,
+                                                           s * 128 + r * pitch, 0);
+        }
+    };
+    auto stage = [&](int buf, auto from) {
+        constexpr int F = decltype(from)::value;
+#pragma unroll
+        for (int i = F; i < F + 8; ++i) data[buf][lrow + 32 * i][chunk ^ (lrow & 7)] = raw[i];
+    };
+    // scales as in the kernel above: of SPAN steps at a time, a quarter of the rows each step, here two rows a lane
+    u32x2 sraw[2];
+    const int spart = tid & 3;
+    auto scale_at = [&](int group) {
+        const int b = 8 * (SPAN * group + spart);
+        return b < blocks ? b : blocks & ~7;
+    };
+    auto fetch_scales = [&](int group, int part, u32x2 (&sraw)[2]) {
+        const int want = scale_at(group), at = want + 8 <= blocks ? want : blocks - 8;
+        const uint8_t* p = part >= 2 ? a.xscales + (long long)m0 * blocks : a.scales + (long long)k0 * blocks;
+        const int most = (part >= 2 ? mrows : krows) - 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 128 * (part & 1) + 64 * i + (tid >> 2);
+            sraw[i] = *(const u32x2_any*)(p + (uint32_t)(r < most ? r : most) * (uint32_t)blocks + at);
+        }
+    };
+    auto stage_scales = [&](int group, int part, const u32x2 (&sraw)[2]) {
+        const int want = scale_at(group), gone = want + 8 <= blocks ? 0 : want - (blocks - 8);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t u = (__builtin_bit_cast(uint64_t, sraw[i]) >> (4 * gone)) >> (4 * gone);
+            scale[group & 1][spart][128 * part + 64 * i + (tid >> 2)] = __builtin_bit_cast(u32x2, u);
+        }
+    };
+    f32x16 acc[R][R];
+    const std::integral_constant<int, 0> zero;
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 3> three;
+    const std::integral_constant<int, 8> eight;
+    struct Operands {
+        u32x4 k[R], m[R];
+    };
+    auto read = [&](int buf, int j, Operands& f) {
+        const int place = (4 * half + j) ^ (sub & 7);
+#pragma unroll
+        for (int i = 0; i < R; ++i) f.k[i] = data[buf][wk + 32 * i + sub][place];
+#pragma unroll
+        for (int i = 0; i < R; ++i) f.m[i] = data[buf][TILE + wm + 32 * i + sub][place];
+    };
+    uint32_t sk[R], sm[R];
+    auto read_scales = [&](int s, uint32_t (&k)[R], uint32_t (&m)[R]) {
+        const u32x2* sp = scale[s / SPAN & 1][s % SPAN];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            k[i] = sp[wk + 32 * i + sub][half];
+            m[i] = sp[TILE + wm + 32 * i + sub][half];
+        }
+    };
+    auto multiply = [&](const Operands& f, auto which) {
+        constexpr int J = decltype(which)::value;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(f.k[i]), fp4_operand(f.m[j]), acc[i][j], 4, 4, J, sk[i], J, sm[j]);
+    };
+    fetch(0, zero);
+    fetch(0, eight);
+    u32x2 all[SPAN][2];
+#pragma unroll
+    for (int q = 0; q < SPAN; ++q) fetch_scales(0, q, all[q]);
+    stage(0, zero);
+    stage(0, eight);
+    // (in the loop's order, by which the compiler counts what it waits for)
+    fetch_scales(1, 0, sraw);
+    fetch(steps > 1 ? 1 : 0, zero);
+    fetch(steps > 1 ? 1 : 0, eight);
+#pragma unroll
+    for (int q = 0; q < SPAN; ++q) stage_scales(0, q, all[q]);
+    __syncthreads();
+    Operands f, g;
+    read(0, 0, f);
+    read_scales(0, sk, sm);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < R; ++j) acc[i][j] = f32x16{};
+    for (int s = 0; s < steps; ++s) {
+        // (without branches: the last steps load and store once more)
+        const int buf = s & 1, then = s + 2 < steps ? s + 2 : steps - 1;
+        read(buf, 1, g);
+        stage(buf ^ 1, zero);
+        multiply(f, zero);
+        order<kLdsRead, kLdsWrite>();
+        read(buf, 2, f);
+        stage(buf ^ 1, eight);
+        stage_scales(s / SPAN + 1, s % SPAN, sraw);
+        multiply(g, one);
+        order<kLdsRead, kLdsWrite>();
+        read(buf, 3, g);
+        fetch_scales((s + 1) / SPAN + 1, (s + 1) % SPAN, sraw);
+        fetch(then, zero);
+        multiply(f, two);
+        order<kLdsRead, kLoad>();
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        read(buf ^ 1, 0, f);
+        uint32_t nk[R], nm[R];
+        read_scales(s + 1, nk, nm);
+        fetch(then, eight);
+        multiply(g, three);
+        order<kLdsRead, kLoad>();
+#pragma unroll
+        for (int i = 0; i < R; ++i) sk[i] = nk[i], sm[i] = nm[i];
+    }
+    float* bias = (float*)&data[1][0][0];
+    stage_bias(a, bias, TILE, k0);
+    store_tiles<T, R, R>(a, acc, (T*)&data[0][0][0] + wave * 32 * (32 * R + 8), bias + wk, m0 + wm, k0 + wk);
+    static_assert(4 * 32 * (32 * R + 8) * (int)sizeof(T) <= (int)sizeof(data[0]), "the outputs' LDS");
+}
+
+// A few tokens (16 MT): the waves share the channels as in mx4_kernel, tokens are loaded as output channels are.
+template <typename T, int MT, int RT, int NW>
+__global__ __launch_bounds__(64 * NW) void mx4x4_few_kernel(Mx4Args a) {
+    constexpr int TILES = RT + MT;
+    __shared__ u32x4 stage[NW][TILES > RT * MT ? TILES : RT * MT][64];
+    auto part = [&](int w, int r, int m) { return (f32x4*)stage[w] + (r * MT + m) * 64; };
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int sub = lane & 15, grp = lane >> 4;
+    const int blocks = a.C / 32, steps = (blocks + 3) / 4;
+    const int k0 = blockIdx.x * (16 * RT), m0 = blockIdx.y * (16 * MT);
+    const int lrow = lane >> 2, lchunk = (lane & 3) ^ (lrow >> 2);
+    const int krows = a.K - k0 < 16 * RT ? a.K - k0 : 16 * RT;
+    const int mrows = a.M - m0 < 16 * MT ? a.M - m0 : 16 * MT;
+    const uint32_t pitch = a.C / 2;
+    const __amdgpu_buffer_rsrc_t rq = mm::rsrc(a.q + (long long)k0 * pitch, krows * pitch);
+    const __amdgpu_buffer_rsrc_t rx = mm::rsrc((const uint8_t*)a.x + (long long)m0 * pitch, mrows * pitch);
+    const __amdgpu_buffer_rsrc_t rs = mm::rsrc(a.scales + (long long)k0 * blocks, (uint32_t)krows * blocks);
+    const __amdgpu_buffer_rsrc_t rt = mm::rsrc(a.xscales + (long long)m0 * blocks, (uint32_t)mrows * blocks);
+    struct Step {
+        u32x4 w[TILES];
+        uint32_t scale[TILES];
+    };
+    auto fetch = [&](int s, Step& v) {
+        const bool in = s * 4 + lchunk < blocks, mine = s * 4 + grp < blocks;
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) {
+            const int row = 16 * (r < RT ? r : r - RT);
+            const uint32_t at = (row + lrow) * pitch + 16 * lchunk, sat = (row + sub) * (uint32_t)blocks + grp;
+            v.w[r] = __builtin_amdgcn_raw_buffer_load_b128(r < RT ? rq : rx, in ? at : mm::kOob, s * (kStep / 2), 0);
+            v.scale[r] = __builtin_amdgcn_raw_buffer_load_b8(r < RT ? rs : rt, mine ? sat : mm::kOob, s * 4, 0);
+        }
+    };
+    f32x4 total[RT][MT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) total[r][m] = f32x4{};
+    const int place = sub * 4 + (grp ^ (sub >> 2));
+    const int last = steps - 1;
+    auto at_most = [&](int s) { return s < last ? s : last; };
+    Step v;
+    fetch(at_most(wave), v);
+    for (int s = wave; s < steps; s += NW) {
+        uint32_t scale[TILES];
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) {
+            stage[wave][r][lane] = v.w[r];
+            scale[r] = v.scale[r];
+        }
+        fetch(at_most(s + NW), v);
+        __builtin_amdgcn_wave_barrier();
+        i32x8 f[TILES];
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) f[r] = fp4_operand(stage[wave][r][place]);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                total[r][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f[RT + m], f[r], total[r][m], 4, 4, 0, scale[RT + m], 0, scale[r]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) part(wave, r, m)[lane] = total[r][m];
+    __syncthreads();
+    const Act act = act_bounds(a.act);
+    for (int j = threadIdx.x; j < RT * MT * 64; j += 64 * NW) {
+        const int l = j & 63, m = (j >> 6) % MT, r = (j >> 6) / MT;
+        const int k = k0 + 16 * r + (l & 15);
         if (k >= a.K) continue;
+        f32x4 v = part(0, r, m)[l];
+#pragma unroll
+        for (int q = 1; q < NW; ++q) v += part(q, r, m)[l];
         const float bias = a.bias ? a.bias[k] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int m = m0 + 16 * i + 4 * grp + e;
-                if (m < a.M) ((T*)a.y)[(long long)m * a.ldy + k] = (T)clamp_act(acc[i][j][e] + bias, act);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int t = m0 + 16 * m + 4 * (l >> 4) + i;
+            if (t < a.M) ((T*)a.y)[(long long)t * a.ldy + k] = (T)clamp_act(v[i] + bias, act);
+        }
     }
 }
 
@@ -382,9 +780,35 @@ int dequantize(const Mx4Args& a, hipStream_t s) {
 }
 template <typename T>
 int product(const Mx4Args& a, hipStream_t s) {
-    const int ktiles = (a.K + 127) / 128;
-    mx4x4_kernel<T><<<(a.M + 127) / 128 * ktiles, 256, 0, s>>>(a, ktiles);
-    return (int)hipGetLastError();
+    using std::integral_constant;
+    auto few = [&](auto mt, auto rt, auto nw) {
+        constexpr int MT = decltype(mt)::value, RT = decltype(rt)::value, NW = decltype(nw)::value;
+        const dim3 grid((a.K + 16 * RT - 1) / (16 * RT), (a.M + 16 * MT - 1) / (16 * MT));
+        mx4x4_few_kernel<T, MT, RT, NW><<<grid, 64 * NW, 0, s>>>(a);
+        return (int)hipGetLastError();
+    };
+    auto tiles = [&](auto wk, auto wm, auto rk, auto rm) {
+        constexpr int WK = decltype(wk)::value, WM = decltype(wm)::value, RK = decltype(rk)::value, RM = decltype(rm)::value;
+        const int ktiles = (a.K + 32 * WK * RK - 1) / (32 * WK * RK), mtiles = (a.M + 32 * WM * RM - 1) / (32 * WM * RM);
+        mx4x4_kernel<T, WK, WM, RK, RM><<<ktiles * mtiles, 64 * WK * WM, 0, s>>>(a, mtiles, ktiles);
+        return (int)hipGetLastError();
+    };
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const integral_constant<int, 4> four;
+    const integral_constant<int, 8> eight;
+    if (a.M <= 64) {
+        const long long rows = (a.K + 15) / 16;
+        if (a.M <= 16) return rows >= 1024 ? few(one, two, four) : few(one, one, eight);
+        if (a.M <= 32) return rows >= 1024 ? few(two, two, four) : few(two, one, eight);
+        return rows >= 1024 ? few(four, two, four) : few(four, one, eight);
+    }
+    const int ktiles = (a.K + 255) / 256, mtiles = (a.M + 255) / 256;
+    if ((long long)ktiles * mtiles >= 192 && a.C >= 256) {
+        mx4x4_large_kernel<T><<<ktiles * mtiles, 256, 0, s>>>(a, mtiles, ktiles);
+        return (int)hipGetLastError();
+    }
+    return tiles(two, two, two, two);
 }
 
 }  // namespace

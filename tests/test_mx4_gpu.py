@@ -130,7 +130,8 @@ def test_products_of_16_bit_tokens(dtype, M, C, K):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("M,C,K", SHAPES + [(300, 416, 290), (129, 1024, 513), (256, 256, 256), (1, 64, 300), (257, 32, 1)])
+@pytest.mark.parametrize("M,C,K", SHAPES + [(300, 416, 290), (129, 1024, 513), (256, 256, 256), (1, 64, 300), (257, 32, 1),
+                                            (3300, 288, 3700), (500, 2336, 300)])
 def test_products_of_4_bit_tokens(dtype, M, C, K):
     import depthwise_pointwise_convolution_amd as F
     g = torch.Generator().manual_seed(M + 3 * C + K)
