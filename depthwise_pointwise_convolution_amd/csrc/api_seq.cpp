@@ -425,6 +425,9 @@ fcm_status fcm_delta_fwd(const fcm_delta_problem* prob, const void* q, const voi
     SEQ_TRY(sequences(prob->tokens, prob->seqs, prob->slots, cu, slots, carry, state));
     DeltaArgs args;
     SEQ_TRY(delta_args(prob, q, k, v, a, b, A, dt_bias, norm, z, slots, state, y, &args));
+    // (a chunk's 64 rows are one 32-bit range)
+    if (args.ldv >= (1 << 22) || args.ldz >= (1 << 22) || args.ldy >= (1 << 22))
+        return unsupported("ldv, ldz or ldy of 2^22 or more");
     NEED(workspace, 16);
     args.cu = cu;
     args.carry = carry;

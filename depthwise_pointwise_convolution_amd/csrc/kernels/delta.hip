@@ -19,7 +19,9 @@
 // (not the state) leave out those below 2^-16.  Quotients G_i / G_j are exponentials of differences of sums
 // held in 64 bits: in 32 the difference of two sums of a few hundred would be off by 2^-16.
 #include <float.h>
+#include <limits.h>
 
+#include "mm_common.h"
 #include "seq_common.h"
 #include "../seq.h"
 
@@ -64,6 +66,22 @@ __device__ __forceinline__ f32x4 mm_pieces(const u32x4* a, const u32x4* b, f32x4
         for (int p = 0; p < NA; ++p)
             if (s - p >= 0 && s - p < NB) acc = mfma<__bf16>(a[p], b[s - p], acc);
     return acc;
+}
+
+// The same from zero in two chains of half the length: a product that adds to the one before waits for it.
+template <int NA, int NB, int KEEP>
+__device__ __forceinline__ f32x4 mm_pieces2(const u32x4* a, const u32x4* b) {
+    f32x4 acc[2] = {};
+    int n = 0;
+#pragma unroll
+    for (int s = KEEP - 1; s >= 0; --s)
+#pragma unroll
+        for (int p = 0; p < NA; ++p)
+            if (s - p >= 0 && s - p < NB) {
+                acc[n & 1] = mfma<__bf16>(a[p], b[s - p], acc[n & 1]);
+                ++n;
+            }
+    return acc[0] + acc[1];
 }
 
 // What the first kernel leaves for the second: for each chunk and key head the operands of K, Q (tokens x
@@ -146,7 +164,7 @@ __device__ __forceinline__ void st_operand(char* p, u32x4 v) {
 
 // One workgroup per chunk and key head.
 template <typename T, int NKB>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
     constexpr int PI = Pieces<T>::IN, PQ = Pieces<T>::OUT, DK = 32 * NKB, LD = DK + 8, LM = 68;
     constexpr int kIn = 2 * kChunk * LD * (int)sizeof(T), kMat = 2 * kChunk * LM * 4;
     __shared__ __attribute__((aligned(16))) char smem[kIn > kMat ? kIn : kMat];
@@ -166,6 +184,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
     const int t0 = seq_offset(a.cu, b, a.tokens) + (id - first_chunk(a.cu, b, a.tokens)) * kChunk;
     const int end = seq_offset(a.cu, b + 1, a.tokens);
     if (id < first_chunk(a.cu, b, a.tokens) || t0 >= end) return;
+    if (end - seq_offset(a.cu, b, a.tokens) <= a.shortest) return;
     const int n = end - t0 < kChunk ? end - t0 : kChunk;
     const int tid = threadIdx.x, lane = tid & 63, sub = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -380,193 +399,453 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
     }
 }
 
-// One workgroup per sequence, value head and slice of 16 NT columns; wave w has the tokens of tile w of each
-// chunk and the state's channels of k-blocks w, w + 4.
+// N neighbouring columns of a state's row, from `c` on; behind the last any (what is computed with them is not stored).
+template <int N>
+__device__ __forceinline__ void load_state(const float* row, int c, int most, bool wide, float* out) {
+    if (N == 2 && wide) {  // (an even number of columns)
+        const float2 v = *(const float2*)(row + (c < most ? c : most - 2));
+        out[0] = v.x;
+        out[N - 1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = row[c + i < most ? c + i : most - 1];
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_state(float* row, int c, int most, bool wide, const float* in) {
+    if (N == 2 && wide) {
+        if (c < most) *(float2*)(row + c) = float2{in[0], in[N - 1]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c + i < most) row[c + i] = in[i];
+    }
+}
+
+// A lane's four rows of a chunk and N neighbouring columns of a tensor of tokens.  The chunk's rows are a range of
+// their own: what is behind the last row reads as zero and is not stored, and a column behind the last has no place.
+template <typename T, int N>
+struct ChunkRows {
+    uint32_t at[N], step;
+    uint32_t row;  // bytes from the head's first row
+    const char* base;
+    long long ld;
+    bool wide;
+    __device__ __forceinline__ ChunkRows(const void* p, long long ld_, long long column, int col, int most, int tok, bool wide_) {
+        base = (const char*)p + column * (long long)sizeof(T);
+        ld = ld_ * (long long)sizeof(T);
+        step = (uint32_t)ld;
+        wide = wide_;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            at[i] = col + i < most ? (uint32_t)tok * step + (uint32_t)(col + i) * (uint32_t)sizeof(T) : mm::kOob;
+        row = (uint32_t)most * (uint32_t)sizeof(T);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t range(int t0, int end) const {
+        const int n = end - t0 < kChunk ? end - t0 : kChunk;
+        return mm::rsrc(base + t0 * ld, (uint32_t)(n - 1) * step + row);
+    }
+    __device__ __forceinline__ void load(int t0, int end, T (&v)[4][N]) const {
+        const __amdgpu_buffer_rsrc_t r = range(t0, end);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (N == 2 && wide) {
+                if constexpr (sizeof(T) == 4) {
+                    const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(r, at[0], i * step, 0);
+                    // (a bit cast of a vector's element takes the first one)
+                    const uint32_t low = x[0], high = x[1];
+                    v[i][0] = __builtin_bit_cast(T, low), v[i][N - 1] = __builtin_bit_cast(T, high);
+                } else {
+                    const uint32_t x = __builtin_amdgcn_raw_buffer_load_b32(r, at[0], i * step, 0);
+                    v[i][0] = __builtin_bit_cast(T, (uint16_t)x), v[i][N - 1] = __builtin_bit_cast(T, (uint16_t)(x >> 16));
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < N; ++t) {
+                    if constexpr (sizeof(T) == 4)
+                        v[i][t] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, at[t], i * step, 0));
+                    else
+                        v[i][t] = __builtin_bit_cast(T, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at[t], i * step, 0));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(int t0, int end, const f32x4 (&o)[N]) const {
+        const __amdgpu_buffer_rsrc_t r = range(t0, end);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (N == 2 && wide) {
+                const T x = (T)o[0][i], y = (T)o[N - 1][i];
+                if constexpr (sizeof(T) == 4)
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)}, r, at[0], i * step, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint16_t, x) | (uint32_t)__builtin_bit_cast(uint16_t, y) << 16, r, at[0], i * step, 0);
+            } else {
+#pragma unroll
+                for (int t = 0; t < N; ++t) {
+                    const T x = (T)o[t][i];
+                    if constexpr (sizeof(T) == 4)
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, at[t], i * step, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, x), r, at[t], i * step, 0);
+                }
+            }
+        }
+    }
+};
+
+// The sum of a row of 16 lanes, in each of them.
+__device__ __forceinline__ float sum16(float v) {
+#define FCM_DPP_ADD(ctrl)                                                                         \
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, 0xf, 0xf, true))
+    FCM_DPP_ADD(0xb1);   // neighbours of a pair, of a quad, the halves of eight, of sixteen
+    FCM_DPP_ADD(0x4e);
+    FCM_DPP_ADD(0x141);
+    FCM_DPP_ADD(0x140);
+#undef FCM_DPP_ADD
+    return v;
+}
+
+// The i-th sequence of more than `shortest` tokens, or -1.
+__device__ __forceinline__ int long_sequence(const int32_t* cu, int seqs, int shortest, int i) {
+    if (shortest < 0) return i;
+    const int lane = threadIdx.x & 63;
+    for (int b = 0; b < seqs; b += 64) {
+        const bool in = b + lane < seqs && cu[b + lane + 1] - cu[b + lane] > shortest;
+        uint64_t who = __ballot(in);
+        const int n = __popcll(who);
+        if (i < n) {
+            for (; i > 0; --i) who &= who - 1;
+            return b + __ffsll((unsigned long long)who) - 1;
+        }
+        i -= n;
+    }
+    return -1;
+}
+// More tokens than `shortest` have at most so many sequences.
+int long_sequences(int seqs, int tokens, int shortest) {
+    return shortest < 0 || seqs < tokens / (shortest + 1) ? seqs : tokens / (shortest + 1);
+}
+
+// One workgroup per sequence, value head and slice of 16 NT columns, NT neighbouring ones a lane.
+//
+// A chunk is a chain: the state as an operand, what the values differ by, U, the new state, each through LDS.  Four
+// waves do only that: wave w has the tokens of tile w of each chunk and the state's channels of k-blocks w, w + 4.
+// Four more have the same tokens' outputs, from the same state and U, beside it.  What a wave reads of the next
+// chunk is loaded as soon as this one is done with the registers.
 template <typename T, int NKB, int NT>
-__global__ __launch_bounds__(256) void delta_chunks_kernel(DeltaArgs a, int slices) {
+__global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slices) {
     constexpr int PI = Pieces<T>::IN, PQ = Pieces<T>::OUT, KW = (NKB + 3) / 4;
-    __shared__ u32x4 sb[NKB][NT][3][64];  // the state as an operand over channels
+    __shared__ u32x4 sb[NKB][NT][PQ][64];  // the state as an operand over channels
+    __shared__ f32x4 parts[4][4][NT][64];  // k S of each wave's channels, by tiles of tokens
     __shared__ u32x4 rb[2][NT][3][64];    // what the values differ by, over tokens
     __shared__ u32x4 ub[2][NT][PQ][64];   // U
     __shared__ u32x4 ud[2][NT][3][64];    // U with the decay to the chunk's end
     const int tid = threadIdx.x, lane = tid & 63, sub = lane & 15, grp = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+    const bool outputs = __builtin_amdgcn_readfirstlane(tid >> 6) >= 4;
     // the slices of a head, which read the same operands, go to one XCD
     const int xcd = blockIdx.x & 7, rest = blockIdx.x >> 3;
     const int slice = rest % slices, bh = (rest / slices) * 8 + xcd;
-    if (bh >= a.seqs * a.Hv) return;
-    const int b = bh / a.Hv, h = bh % a.Hv, hk = h / (a.Hv / a.Hk);
+    const int b = bh < a.seqs * a.Hv ? long_sequence(a.cu, a.seqs, a.shortest, bh / a.Hv) : -1;
+    if (b < 0) return;
+    const int h = bh % a.Hv, hk = h / (a.Hv / a.Hk);
     const int start = seq_offset(a.cu, b, a.tokens), end = seq_offset(a.cu, b + 1, a.tokens);
-    const int slot = a.state ? seq_slot(a.slots, b, a.nslots) : -1;
     const Layout lay = layout(PI, PQ, NKB);
+    const int col = (slice * 16 + sub) * NT;
+    const long long hv = (long long)h * a.Dv;
+    const int tok = 32 * (wave >> 1) + 8 * grp + 4 * (wave & 1);  // this lane's tokens of a chunk: .. + i
+    const long long key_step = a.Hk * lay.key_bytes, head_step = a.Hv * lay.head_bytes;
+    const int first = first_chunk(a.cu, b, a.tokens);
+    const char* key = (const char*)a.ws + first * key_step + hk * lay.key_bytes;
+    const char* head = (const char*)a.ws + a.places * key_step + first * head_step + h * lay.head_bytes;
+    // the lower operands of tile `wave`: columns that lie above the first tiles' rows read as zero
+    auto lower_operand = [&](const __amdgpu_buffer_rsrc_t& r, long long from, int p, int kb) {
+        return __builtin_amdgcn_raw_buffer_load_b128(
+            r, kb <= (wave >> 1) ? (int)(from + (p * 6 + lower(wave, kb)) * kFrag + lane * 16) : (int)mm::kOob, 0, 0);
+    };
+
+    if (outputs) {
+        const bool gate = !a.norm && a.z;
+        const ChunkRows<T, NT> ys(a.y, a.ldy, hv, col, a.Dv, tok, a.wide_y), zs(a.z, a.ldz, hv, col, a.Dv, tok, a.wide_z);
+        u32x4 q[NKB][PI], pw[2][PQ];
+        f32x4 seen;
+        T z[4][NT];
+        auto load_q = [&]() {
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+                for (int p = 0; p < PI; ++p) q[kb][p] = ld16(key + lay.qf + ((p * 4 + wave) * NKB + kb) * kFrag + lane * 16);
+            seen = *(const f32x4*)((const float*)(head + lay.rows) + kChunk + tok);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto load_weights = [&](int t0) {
+            const __amdgpu_buffer_rsrc_t rh = mm::rsrc(head, (uint32_t)lay.head_bytes);
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int p = 0; p < PQ; ++p) pw[kb][p] = lower_operand(rh, lay.pf, p, kb);
+            if (gate) zs.load(t0, end, z);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if (start < end) {
+            load_q();
+            load_weights(start);
+        }
+        for (int t0 = start; t0 < end; t0 += kChunk) {
+            // (behind the last chunk it is loaded once more)
+            const bool more = t0 + kChunk < end;
+            key += more ? key_step : 0;
+            head += more ? head_step : 0;
+            __syncthreads();
+            __syncthreads();
+            f32x4 o[NT];
+            // (in the chain's second part: in the first it reads more of LDS itself)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                u32x4 f[NKB][PQ];
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+                    for (int p = 0; p < PQ; ++p) f[kb][p] = sb[kb][t][p][lane];
+                __builtin_amdgcn_sched_barrier(0);
+                o[t] = f32x4{};
+#pragma unroll
+                for (int kb = 0; kb < NKB; ++kb) o[t] = mm_pieces<PI, PQ, PQ>(q[kb], f[kb], o[t]);
+                o[t] *= seen;
+            }
+            load_q();
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                u32x4 f[2][PQ];
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int p = 0; p < PQ; ++p) f[kb][p] = ub[kb][t][p][lane];
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) o[t] = mm_pieces<PQ, PQ, PQ>(pw[kb], f[kb], o[t]);
+            }
+            if (gate)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[t][i] *= silu((float)z[i][t]);
+            load_weights(more ? t0 + kChunk : t0);
+            if (a.norm) {
+                float squares[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (col + t < a.Dv) v = __builtin_fmaf(o[t][i], o[t][i], v);
+                    squares[i] = sum16(v);
+                }
+                float* to = a.squares + ((long long)(t0 + tok) * a.Hv + h) * slices + slice;
+                if (sub == 0)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t0 + tok + i < end) to[(long long)i * a.Hv * slices] = squares[i];
+            }
+            ys.store(t0, end, o);
+        }
+        return;
+    }
+
+    __builtin_amdgcn_s_setprio(2);  // the chain before the outputs
+    const int slot = a.state ? seq_slot(a.slots, b, a.nslots) : -1;
     float* state = slot >= 0 ? a.state + ((long long)slot * a.Hv + h) * a.Dk * a.Dv : nullptr;
     const bool carried = state && a.carry && a.carry[b] != 0;
-    int col[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) col[t] = (slice * NT + t) * 16 + sub;
-
     // channel of row r = 4 grp + i of tile half hf of k-block kb: 32 kb + 8 grp + 4 hf + i
     f32x4 S[KW][2][NT];
 #pragma unroll
     for (int k = 0; k < KW; ++k)
 #pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = 32 * (wave + 4 * k) + 8 * grp + 4 * hf + i;
+                float v[NT] = {};
+                if (carried && c < a.Dk) load_state<NT>(state + (long long)c * a.Dv, col, a.Dv, a.wide_state, v);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) S[k][hf][t][i] = v[t];
+            }
+        }
+    // (here, or the loop would wait for its own loads too)
+#pragma unroll
+    for (int k = 0; k < KW; ++k)
+#pragma unroll
         for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) asm volatile("" : "+v"(S[k][hf][t]));
+    const ChunkRows<T, NT> vs(a.v, a.ldv, hv, col, a.Dv, tok, a.wide_v);
+    u32x4 kf[4][KW][PI], kt[KW][2][2][PI], tw[2][3];
+    f32x4 known, left;  // the rows' factors
+    float last;
+    T v[4][NT];
+    // (the compiler would move the loads to their use)
+    auto load_k = [&](int t0) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int k = 0; k < KW; ++k)
+#pragma unroll
+                for (int p = 0; p < PI; ++p) {
+                    // (a wave without channels has nothing to do with these: any will do)
+                    const int kb = wave + 4 * k < NKB ? wave + 4 * k : 0;
+                    kf[m][k][p] = ld16(key + lay.kf + ((p * 4 + m) * NKB + kb) * kFrag + lane * 16);
+                }
+        known = *(const f32x4*)((const float*)(head + lay.rows) + tok);
+        vs.load(t0, end, v);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_inverse = [&]() {
+        const __amdgpu_buffer_rsrc_t rh = mm::rsrc(head, (uint32_t)lay.head_bytes);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int p = 0; p < 3; ++p) tw[kb][p] = lower_operand(rh, lay.tf, p, kb);
+        left = *(const f32x4*)((const float*)(head + lay.rows) + 2 * kChunk + tok);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_kt = [&]() {
+#pragma unroll
+        for (int k = 0; k < KW; ++k)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int p = 0; p < PI; ++p) {
+                        // (a wave without channels has nothing to do with these: any will do)
+                        const int s = wave + 4 * k < NKB ? 2 * (wave + 4 * k) + hf : 0;
+                        kt[k][hf][kb][p] = ld16(key + lay.kt + ((p * 2 * NKB + s) * 2 + kb) * kFrag + lane * 16);
+                    }
+        last = ((const float*)(head + lay.rows))[3 * kChunk];
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (start < end) {
+        load_k(start);
+        load_inverse();
+        load_kt();
+    }
+    for (int t0 = start; t0 < end; t0 += kChunk) {
+        const bool more = t0 + kChunk < end;
+        key += more ? key_step : 0;
+        head += more ? head_step : 0;
+        // (the column tiles beside each other: their products wait for none of each other's)
+        {
+            u32x4 f[NT][KW][3];
+            f32x4 ks[NT][4] = {};
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 32 * (wave + 4 * k) + 8 * grp + 4 * hf + i;
-                    S[k][hf][t][i] = carried && c < a.Dk && col[t] < a.Dv ? state[(long long)c * a.Dv + col[t]] : 0.0f;
+                for (int k = 0; k < KW; ++k) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = S[k][i >> 2][t][i & 3];
+                    split8<3>(x, f[t][k]);
                 }
-    int place = first_chunk(a.cu, b, a.tokens);
-    for (int t0 = start; t0 < end; t0 += kChunk, ++place) {
-        const char* key = (const char*)a.ws + ((long long)place * a.Hk + hk) * lay.key_bytes;
-        const char* head = (const char*)a.ws + a.places * a.Hk * lay.key_bytes +
-                           ((long long)place * a.Hv + h) * lay.head_bytes;
-        const float* rows = (const float*)(head + lay.rows);
-        const int tok = 32 * (wave >> 1) + 8 * grp + 4 * (wave & 1);  // .. + i
 #pragma unroll
-        for (int k = 0; k < KW; ++k)
-            if (wave + 4 * k < NKB)
+            for (int s = 2; s >= 0; --s)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    float v[8];
+                for (int k = 0; k < KW; ++k)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = S[k][i >> 2][t][i & 3];
-                    u32x4 f[3];
-                    split8<3>(v, f);
+                    for (int p = 0; p < PI; ++p)
+                        if (s - p >= 0)
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) sb[wave + 4 * k][t][p][lane] = f[p];
-                }
-        __syncthreads();
-        f32x4 ks[NT], o[NT];
+                            for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) ks[t] = o[t] = f32x4{};
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-            u32x4 fk[PI], fq[PI];
-#pragma unroll
-            for (int p = 0; p < PI; ++p) {
-                fk[p] = ld16(key + lay.kf + ((p * 4 + wave) * NKB + kb) * kFrag + lane * 16);
-                fq[p] = ld16(key + lay.qf + ((p * 4 + wave) * NKB + kb) * kFrag + lane * 16);
-            }
+                                for (int m = 0; m < 4; ++m) ks[t][m] = mfma<__bf16>(kf[m][k][p], f[t][k][s - p], ks[t][m]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                u32x4 f[3];
 #pragma unroll
-                for (int p = 0; p < 3; ++p) f[p] = sb[kb][t][p][lane];
-                ks[t] = mm_pieces<PI, 3, 3>(fk, f, ks[t]);
-                o[t] = mm_pieces<PI, 3, PQ>(fq, f, o[t]);
+                for (int m = 0; m < 4; ++m) parts[wave][m][t][lane] = ks[t][m];
+#pragma unroll
+                for (int k = 0; k < KW; ++k)
+                    if (NKB % 4 == 0 || wave + 4 * k < NKB)
+#pragma unroll
+                        for (int p = 0; p < PQ; ++p) sb[wave + 4 * k][t][p][lane] = f[t][k][p];
             }
         }
+        __syncthreads();
+        // (all reads, then what follows: the compiler would wait for each)
+        f32x4 ks[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int w = 0; w < 4 && w < NKB; ++w) ks[t][w] = parts[w][wave][t][lane];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             float r[8] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int m = tok + i;
-                float v = 0.0f;
-                if (t0 + m < end && col[t] < a.Dv)
-                    v = (float)((const T*)a.v)[(t0 + m) * a.ldv + (long long)h * a.Dv + col[t]];
-                r[i] = __builtin_fmaf(-rows[m], ks[t][i], v);
-                o[t][i] *= rows[kChunk + m];
-            }
-            u32x4 f[3];
-            split8<3>(r, f);
+            for (int w = 1; w < 4 && w < NKB; ++w) ks[t][0] += ks[t][w];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = __builtin_fmaf(-known[i], ks[t][0][i], (float)v[i][t]);
+            u32x4 g[3];
+            split8<3>(r, g);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
-                *(uint2*)((char*)&rb[wave >> 1][t][p][lane] + 8 * (wave & 1)) = uint2{f[p][0], f[p][1]};
+                *(u32x2*)((char*)&rb[wave >> 1][t][p][lane] + 8 * (wave & 1)) = u32x2{g[p][0], g[p][1]};
         }
+        load_k(more ? t0 + kChunk : t0);
         __syncthreads();
-        f32x4 u[NT];
+        f32x4 us[NT];
+        {
+            u32x4 f[NT][2][3];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) u[t] = f32x4{};
-        for (int kb = 0; kb <= (wave >> 1); ++kb) {
-            u32x4 ft[3];
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int p = 0; p < 3; ++p) ft[p] = ld16(head + lay.tf + (p * 6 + lower(wave, kb)) * kFrag + lane * 16);
+                for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                u32x4 f[3];
+                    for (int p = 0; p < 3; ++p) f[t][kb][p] = rb[kb][t][p][lane];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int p = 0; p < 3; ++p) f[p] = rb[kb][t][p][lane];
-                u[t] = mm_pieces<3, 3, 3>(ft, f, u[t]);
-            }
+            for (int t = 0; t < NT; ++t)
+                us[t] = mm_pieces2<3, 3, 3>(tw[0], f[t][0]) + mm_pieces2<3, 3, 3>(tw[1], f[t][1]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            float v[8] = {}, w[8] = {};
+            const f32x4 u = us[t];
+            float x[8] = {}, w[8] = {};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[i] = u[t][i];
-                w[i] = u[t][i] * rows[2 * kChunk + tok + i];
+                x[i] = u[i];
+                w[i] = u[i] * left[i];
             }
-            u32x4 f[3];
-            split8<PQ>(v, f);
-#pragma unroll
-            for (int p = 0; p < PQ; ++p)
-                *(uint2*)((char*)&ub[wave >> 1][t][p][lane] + 8 * (wave & 1)) = uint2{f[p][0], f[p][1]};
-            split8<3>(w, f);
+            u32x4 g[3];
+            split8<3>(w, g);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
-                *(uint2*)((char*)&ud[wave >> 1][t][p][lane] + 8 * (wave & 1)) = uint2{f[p][0], f[p][1]};
+                *(u32x2*)((char*)&ud[wave >> 1][t][p][lane] + 8 * (wave & 1)) = u32x2{g[p][0], g[p][1]};
+            split8<PQ>(x, g);
+#pragma unroll
+            for (int p = 0; p < PQ; ++p)
+                *(u32x2*)((char*)&ub[wave >> 1][t][p][lane] + 8 * (wave & 1)) = u32x2{g[p][0], g[p][1]};
         }
+        load_inverse();
         __syncthreads();
-        const float last = rows[3 * kChunk];
+        {
+            u32x4 f[NT][2][3];
 #pragma unroll
-        for (int k = 0; k < KW; ++k)
-            if (wave + 4 * k < NKB)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) S[k][hf][t] *= last;
+                    for (int p = 0; p < 3; ++p) f[t][kb][p] = ud[kb][t][p][lane];
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int kb = 0; kb < 2; ++kb) {
-                        u32x4 fk[PI];
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int p = 0; p < PI; ++p)
-                            fk[p] = ld16(key + lay.kt + ((p * 2 * NKB + 2 * (wave + 4 * k) + hf) * 2 + kb) * kFrag + lane * 16);
+                for (int k = 0; k < KW; ++k)
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            u32x4 f[3];
-#pragma unroll
-                            for (int p = 0; p < 3; ++p) f[p] = ud[kb][t][p][lane];
-                            S[k][hf][t] = mm_pieces<PI, 3, 3>(fk, f, S[k][hf][t]);
-                        }
-                    }
-                }
-        for (int kb = 0; kb <= (wave >> 1); ++kb) {
-            u32x4 fp[PQ];
-#pragma unroll
-            for (int p = 0; p < PQ; ++p) fp[p] = ld16(head + lay.pf + (p * 6 + lower(wave, kb)) * kFrag + lane * 16);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                u32x4 f[PQ];
-#pragma unroll
-                for (int p = 0; p < PQ; ++p) f[p] = ub[kb][t][p][lane];
-                o[t] = mm_pieces<PQ, PQ, PQ>(fp, f, o[t]);
-            }
+                    for (int hf = 0; hf < 2; ++hf)
+                        S[k][hf][t] = mm_pieces<PI, 3, 3>(kt[k][hf][0], f[t][0], S[k][hf][t] * last) +
+                                      mm_pieces<PI, 3, 3>(kt[k][hf][1], f[t][1], f32x4{});
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = t0 + tok + i;
-            if (m >= end) continue;
-            float squares = 0.0f;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (col[t] >= a.Dv) continue;
-                float v = o[t][i];
-                squares = __builtin_fmaf(v, v, squares);
-                const long long at = (long long)h * a.Dv + col[t];
-                if (!a.norm && a.z) v *= silu((float)((const T*)a.z)[m * a.ldz + at]);
-                ((T*)a.y)[m * a.ldy + at] = (T)v;
-            }
-            if (a.norm) {
-#pragma unroll
-                for (int s = 1; s < 16; s <<= 1) squares += __shfl_xor(squares, s);
-                if (sub == 0) a.squares[((long long)m * a.Hv + h) * slices + slice] = squares;
-            }
-        }
+        load_kt();
     }
     if (!state) return;
 #pragma unroll
@@ -574,182 +853,279 @@ __global__ __launch_bounds__(256) void delta_chunks_kernel(DeltaArgs a, int slic
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int i = 0; i < 4; ++i) {
+                const int c = 32 * (wave + 4 * k) + 8 * grp + 4 * hf + i;
+                float x[NT];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 32 * (wave + 4 * k) + 8 * grp + 4 * hf + i;
-                    if (c < a.Dk && col[t] < a.Dv) state[(long long)c * a.Dv + col[t]] = S[k][hf][t][i];
-                }
+                for (int t = 0; t < NT; ++t) x[t] = S[k][hf][t][i];
+                if (c < a.Dk) store_state<NT>(state + (long long)c * a.Dv, col, a.Dv, a.wide_state, x);
+            }
 }
 
-// The output's norm and gate, in place: the second kernel's slices left their sums of squares.  A wave per row
-// and head.
-template <typename T>
-__global__ __launch_bounds__(256) void delta_norm_kernel(DeltaArgs a, int slices) {
-    const int lane = threadIdx.x & 63;
-    const long long id = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const long long t = id / a.Hv, h = id % a.Hv;
-    if (t < seq_offset(a.cu, 0, a.tokens) || t >= seq_offset(a.cu, a.seqs, a.tokens)) return;
-    float s = 0.0f;
-    for (int i = 0; i < slices; ++i) s += a.squares[id * slices + i];
-    const float f = 1.0f / __builtin_sqrtf(s / (float)a.Dv + a.eps);
-    T* y = (T*)a.y + t * a.ldy + h * a.Dv;
-    const T* z = a.z ? (const T*)a.z + t * a.ldz + h * a.Dv : nullptr;
-    for (int c = lane; c < a.Dv; c += 64) {
-        float v = (float)y[c] * f * a.norm[c];
-        if (z) v *= silu((float)z[c]);
-        y[c] = (T)v;
+// The output's norm and gate, in place: the second kernel's slices left their sums of squares, a negative one the
+// short sequences' kernel, which has done it all.  A group of `width` lanes has kNormRows rows of heads, one after the
+// other in memory, whose loads are all under way before the first is used.
+constexpr int kNormRows = 4;
+template <typename T, bool WIDE>
+__global__ __launch_bounds__(256) void delta_norm_kernel(DeltaArgs a, int slices, int width) {
+    constexpr int VE = Vec<T>::N;
+    const int x = threadIdx.x & (width - 1), groups = 256 / width;
+    // (tokens * Hv is below 2^26, or the launch would not be)
+    const uint32_t first = (uint32_t)blockIdx.x * (groups * kNormRows) + threadIdx.x / width;
+    const int from = seq_offset(a.cu, 0, a.tokens), to = seq_offset(a.cu, a.seqs, a.tokens);
+    T* y[kNormRows];
+    u32x4 vy[kNormRows], vz[kNormRows];
+    float s[kNormRows], norm[VE];
+    bool live[kNormRows];
+    const int c = x * VE;  // (WIDE: a row has no more vectors than lanes)
+#pragma unroll
+    for (int r = 0; r < kNormRows; ++r) {
+        const uint32_t id = first + r * groups;
+        const long long t = id / (uint32_t)a.Hv;
+        const int h = id - (uint32_t)t * a.Hv;
+        live[r] = t >= from && t < to;
+        if (!live[r]) continue;
+        y[r] = (T*)a.y + t * a.ldy + (long long)h * a.Dv;
+        if (WIDE && c < a.Dv) {
+            vy[r] = ld16(y[r] + c);
+            if (a.z) vz[r] = ld16((const T*)a.z + t * a.ldz + (long long)h * a.Dv + c);
+        }
+        s[r] = a.squares[(long long)id * slices];
+        if (s[r] < 0.0f) live[r] = false;
+        for (int i = 1; i < slices; ++i) s[r] += a.squares[(long long)id * slices + i];
+    }
+    if (WIDE && c < a.Dv)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) norm[i] = a.norm[c + i];
+#pragma unroll
+    for (int r = 0; r < kNormRows; ++r) {
+        if (!live[r]) continue;
+        const float f = 1.0f / __builtin_sqrtf(s[r] / (float)a.Dv + a.eps);
+        if constexpr (WIDE) {
+            if (c >= a.Dv) continue;
+            float v[VE], g[VE];
+            unpack16<T>(vy[r], v);
+            if (a.z) unpack16<T>(vz[r], g);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                v[i] *= f * norm[i];
+                if (a.z) v[i] *= silu(g[i]);
+            }
+            st16(y[r] + c, pack16<T>(v));
+        } else {
+            const uint32_t id = first + r * groups;
+            const long long t = id / (uint32_t)a.Hv;
+            const int h = id - (uint32_t)t * a.Hv;
+            const T* z = a.z ? (const T*)a.z + t * a.ldz + (long long)h * a.Dv : nullptr;
+            for (int i = x; i < a.Dv; i += width) {
+                float v = (float)y[r][i] * f * a.norm[i];
+                if (z) v *= silu((float)z[i]);
+                y[r][i] = (T)v;
+            }
+        }
     }
 }
 
-// Single tokens.  A workgroup has a sequence and a head: lanes along the columns, four each, tx of them, and
-// a.Dk rows over the groups of tx threads, 16 rows each.
-template <typename T, bool WIDE>
-__global__ __launch_bounds__(1024) void delta_step_kernel(DeltaArgs a, int tx, int groups) {
-    __shared__ float vec[2][256];           // q and k with their factors
-    __shared__ float part[2][16][256 + 4];  // the groups' sums over their rows
-    const int tid = threadIdx.x, lane = tid & 63;
+// Tokens one after the other, with the state in registers: the single-token call, and sequences of up to kShort tokens
+// (drafted ones, a prompt's last few) among prompts, for which chunks would read and write 100 KB of operands a head.
+//
+// A workgroup has a sequence and a head, a wave 16 columns of its state: lane l has rows RPL * (l % 16) .. of four columns
+// from 4 * (l / 16) on, so that sums over rows stay within 16 lanes and no wave waits for another.  (With rows over the
+// waves and their sums through LDS, 32 sequences of 5 tokens took 62 us.)  Outputs wait in LDS for the norm, which is over all
+// columns.
+constexpr int kShort = 16;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+// N elements of a row from c on, zero behind the last; they stay in the storage type until they are used.  (A vector
+// access from any element's address is one instruction.)
+template <typename T, int N>
+__device__ __forceinline__ vec_t<T, N> load_some(const T* p, int c, int most) {
+    constexpr int VN = N * sizeof(T) < 16 ? N : 16 / sizeof(T);
+    typedef vec_t<T, VN> V __attribute__((aligned(sizeof(T))));
+    vec_t<T, N> out = {};
+#pragma unroll
+    for (int i = 0; i < N; i += VN) {
+        if (c + i + VN <= most) {
+            const V v = *(const V*)(p + c + i);
+#pragma unroll
+            for (int j = 0; j < VN; ++j) out[i + j] = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < VN; ++j)
+                if (c + i + j < most) out[i + j] = p[c + i + j];
+        }
+    }
+    return out;
+}
+
+template <typename T, int RPL>
+__global__ __launch_bounds__(RPL == 16 ? 512 : 1024) void delta_tokens_kernel(DeltaArgs a, int slices) {
+    __shared__ float outs[kShort][256], squares[kShort][16];
+    const int tid = threadIdx.x, lane = tid & 63, rg = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
     const int b = blockIdx.x / a.Hv, h = blockIdx.x % a.Hv, hk = h / (a.Hv / a.Hk);
-    const int slot = seq_slot(a.slots, b, a.nslots);
-    T* y = (T*)a.y + b * a.ldy + (long long)h * a.Dv;
-    if (slot < 0) {
-        for (int c = tid; c < a.Dv; c += blockDim.x) y[c] = (T)0.0f;
+    const int start = a.cu ? seq_offset(a.cu, b, a.tokens) : b;
+    const int n = a.cu ? seq_offset(a.cu, b + 1, a.tokens) - start : 1;
+    if (n > kShort) return;
+    const long long hv = (long long)h * a.Dv;
+    const int slot = a.state ? seq_slot(a.slots, b, a.nslots) : -1;
+    if (!a.cu && slot < 0) {  // an idle row
+        for (int c = tid; c < a.Dv; c += blockDim.x) ((T*)a.y)[(long long)b * a.ldy + hv + c] = (T)0.0f;
         return;
     }
-    float* state = a.state + ((long long)slot * a.Hv + h) * a.Dk * a.Dv;
-    const int x = tid % tx, rg = tid / tx, c0 = 4 * x;
-    const bool mine = rg < groups;  // (the last wave may be larger)
-    f32x4 S[16];
+    float* state = slot >= 0 ? a.state + ((long long)slot * a.Hv + h) * a.Dk * a.Dv : nullptr;
+    const bool carried = state && (!a.cu || (a.carry && a.carry[b] != 0));
+    const int r0 = RPL * rg, columns = (a.Dv + 15) / 16;
+    const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f, A = a.A[h];
+    for (int block = wave; block < columns; block += waves) {
+        const int c0 = 16 * block + 4 * (lane >> 4);
+        f32x4 S[RPL];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const int r = rg + groups * j;
-        S[j] = f32x4{};
-        if (mine && r < a.Dk) {
-            const float* p = state + (long long)r * a.Dv + c0;
-            if constexpr (WIDE) {
-                S[j] = *(const f32x4*)p;
-            } else {
+        for (int j = 0; j < RPL; ++j) {
+            S[j] = f32x4{};
+            if (carried && r0 + j < a.Dk) S[j] = load_some<float, 4>(state + (long long)(r0 + j) * a.Dv, c0, a.Dv);
+        }
+        vec_t<T, RPL> q, k;
+        vec_t<T, 4> v;
+        T ga, gb;
+        auto load = [&](int t) {
+            const long long row = start + t;
+            q = load_some<T, RPL>((const T*)a.q + row * a.ldq + (long long)hk * a.Dk, r0, a.Dk);
+            k = load_some<T, RPL>((const T*)a.k + row * a.ldk + (long long)hk * a.Dk, r0, a.Dk);
+            v = load_some<T, 4>((const T*)a.v + row * a.ldv + hv, c0, a.Dv);
+            ga = ((const T*)a.a)[row * a.lda + h];
+            gb = ((const T*)a.b)[row * a.ldb + h];
+        };
+        if (n > 0) load(0);
+        for (int t = 0; t < n; ++t) {
+            float fq[RPL], fk[RPL], fv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c0 + i < a.Dv) S[j][i] = p[i];
+            for (int j = 0; j < RPL; ++j) fq[j] = (float)q[j], fk[j] = (float)k[j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fv[i] = (float)v[i];
+            const float alpha = __builtin_amdgcn_exp2f((float)log_decay(ga, bias, A, a.softplus));
+            const float beta = rate_of(gb);
+            if (t + 1 < n) load(t + 1);
+            float qq = 0.0f, kk = 0.0f, qk = 0.0f;
+            f32x4 ks = {}, qs = {};
+#pragma unroll
+            for (int j = 0; j < RPL; ++j) {
+                qq = __builtin_fmaf(fq[j], fq[j], qq);
+                kk = __builtin_fmaf(fk[j], fk[j], kk);
+                qk = __builtin_fmaf(fq[j], fk[j], qk);
+                ks += fk[j] * S[j];
+                qs += fq[j] * S[j];
             }
-        }
-    }
-    // q, k: every wave finds their norms and product for itself, the first one keeps them
-    float qq = 0.0f, kk = 0.0f, qk = 0.0f, qv[4], kv[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = lane + 64 * i;
-        qv[i] = c < a.Dk ? (float)((const T*)a.q)[b * a.ldq + (long long)hk * a.Dk + c] : 0.0f;
-        kv[i] = c < a.Dk ? (float)((const T*)a.k)[b * a.ldk + (long long)hk * a.Dk + c] : 0.0f;
-        qq = __builtin_fmaf(qv[i], qv[i], qq);
-        kk = __builtin_fmaf(kv[i], kv[i], kk);
-        qk = __builtin_fmaf(qv[i], kv[i], qk);
-    }
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        qq += __shfl_xor(qq, s);
-        kk += __shfl_xor(kk, s);
-        qk += __shfl_xor(qk, s);
-    }
-    const float rq = a.scale * (a.qk_norm ? 1.0f / __builtin_sqrtf(qq + a.eps) : 1.0f);
-    const float rk = a.qk_norm ? 1.0f / __builtin_sqrtf(kk + a.eps) : 1.0f;
-    qk *= rq * rk;
-    if (tid < 64)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            vec[0][lane + 64 * i] = qv[i] * rq;
-            vec[1][lane + 64 * i] = kv[i] * rk;
-        }
-    const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-    const float alpha = __builtin_amdgcn_exp2f(
-        (float)log_decay(((const T*)a.a)[b * a.lda + h], bias, a.A[h], a.softplus));
-    const float beta = rate_of(((const T*)a.b)[b * a.ldb + h]);
-    __syncthreads();
-    f32x4 ks = {}, qs = {};
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const int r = rg + groups * j;
-        if (r < a.Dk) {
-            ks += vec[1][r] * S[j];
-            qs += vec[0][r] * S[j];
-        }
-    }
-    if (mine)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            part[0][rg][c0 + i] = ks[i];
-            part[1][rg][c0 + i] = qs[i];
-        }
-    __syncthreads();
-    ks = qs = f32x4{};
-    for (int g = 0; g < groups; ++g) {
-        ks += *(const f32x4*)&part[0][g][c0];
-        qs += *(const f32x4*)&part[1][g][c0];
-    }
-    f32x4 u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float v = c0 + i < a.Dv ? (float)((const T*)a.v)[b * a.ldv + (long long)h * a.Dv + c0 + i] : 0.0f;
-        u[i] = beta * (v - alpha * ks[i]);
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const int r = rg + groups * j;
-        if (mine && r < a.Dk) {
-            const f32x4 now = alpha * S[j] + vec[1][r] * u;
-            float* p = state + (long long)r * a.Dv + c0;
-            if constexpr (WIDE) {
-                *(f32x4*)p = now;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c0 + i < a.Dv) p[i] = now[i];
+            qk = sum16(qk);
+            float rq = a.scale, rk = 1.0f;
+            if (a.qk_norm) {
+                rq /= __builtin_sqrtf(sum16(qq) + a.eps);
+                rk /= __builtin_sqrtf(sum16(kk) + a.eps);
             }
+            f32x4 u;
+            float o[4], sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u[i] = beta * (fv[i] - alpha * (rk * sum16(ks[i])));
+                o[i] = rq * (alpha * sum16(qs[i]) + qk * rk * u[i]);
+                if (c0 + i < a.Dv) sum = __builtin_fmaf(o[i], o[i], sum);
+            }
+            const f32x4 w = rk * u;
+#pragma unroll
+            for (int j = 0; j < RPL; ++j) S[j] = alpha * S[j] + fk[j] * w;
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (rg == 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) outs[t][c0 + i] = o[i];
+            if (lane == 0) squares[t][block] = sum;
+        }
+        if (state)
+#pragma unroll
+            for (int j = 0; j < RPL; ++j) {
+                if (r0 + j >= a.Dk) continue;
+                float* p = state + (long long)(r0 + j) * a.Dv + c0;
+                if (c0 + 4 <= a.Dv) {
+                    *(f32x4_any*)p = S[j];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c0 + i < a.Dv) p[i] = S[j][i];
+                }
+            }
+    }
+    __syncthreads();
+    for (int t = wave; t < n; t += waves) {
+        const long long row = start + t;
+        float f = 1.0f;
+        if (a.norm) {
+            float sum = 0.0f;
+            for (int i = 0; i < columns; ++i) sum += squares[t][i];
+            f = 1.0f / __builtin_sqrtf(sum / (float)a.Dv + a.eps);
+            // (the chunks' norm leaves the row alone)
+            if (slices > 0 && lane == 0) a.squares[(row * a.Hv + h) * slices] = -1.0f;
+        }
+        for (int c = lane; c < a.Dv; c += 64) {
+            float y = outs[t][c];
+            if (a.norm) y *= f * a.norm[c];
+            if (a.z) y *= silu((float)((const T*)a.z)[row * a.ldz + hv + c]);
+            ((T*)a.y)[row * a.ldy + hv + c] = (T)y;
         }
     }
-    if (tid >= 64) return;
-    // the first wave has the output's columns (tx is at most 64)
-    float o[4], squares = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[i] = alpha * qs[i] + qk * u[i];
-        if (rg == 0 && c0 + i < a.Dv) squares = __builtin_fmaf(o[i], o[i], squares);
-    }
-    float f = 1.0f;
-    if (a.norm) {
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) squares += __shfl_xor(squares, s);
-        f = 1.0f / __builtin_sqrtf(squares / (float)a.Dv + a.eps);
-    }
-    if (rg == 0)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = c0 + i;
-            if (c >= a.Dv) continue;
-            float v = o[i];
-            if (a.norm) v *= f * a.norm[c];
-            if (a.z) v *= silu((float)((const T*)a.z)[b * a.ldz + (long long)h * a.Dv + c]);
-            y[c] = (T)v;
-        }
 }
 
 int k_blocks(int Dk) { return Dk <= 32 ? 1 : Dk <= 64 ? 2 : Dk <= 128 ? 4 : 8; }
 int pieces_in(int dtype) { return dtype == FCM_F32 ? 3 : dtype == FCM_F16 ? 2 : 1; }
 int pieces_out(int dtype) { return dtype == FCM_F32 ? 3 : 2; }
 long long chunk_places(int tokens, int seqs) { return (long long)tokens / kChunk + seqs + 1; }
+// Tiles of 16 columns of a workgroup.
+int slice_tiles(int seqs, int Hv, int Dv) { return (long long)seqs * Hv * ((Dv + 31) / 32) >= 512 ? 2 : 1; }
 int column_slices(int Dv, int nt) { return (Dv + 16 * nt - 1) / (16 * nt); }
 
+template <typename T, int NKB, int NT>
+int chunks(const DeltaArgs& a, int slices, hipStream_t s) {
+    const int seqs = long_sequences(a.seqs, a.tokens, a.shortest);
+    delta_chunks_kernel<T, NKB, NT><<<(seqs * a.Hv + 7) / 8 * 8 * slices, 512, 0, s>>>(a, slices);
+    return (int)hipGetLastError();
+}
+
+template <typename T>
+int by_tokens(const DeltaArgs& a, int slices, hipStream_t s) {
+    const int waves = (a.Dv + 15) / 16;
+    if (a.Dk <= 64)
+        delta_tokens_kernel<T, 4><<<a.seqs * a.Hv, 64 * waves, 0, s>>>(a, slices);
+    else if (a.Dk <= 128)
+        delta_tokens_kernel<T, 8><<<a.seqs * a.Hv, 64 * waves, 0, s>>>(a, slices);
+    else
+        delta_tokens_kernel<T, 16><<<a.seqs * a.Hv, 64 * (waves < 8 ? waves : 8), 0, s>>>(a, slices);
+    return (int)hipGetLastError();
+}
+
+// Which sequences are short only the device knows, unless there is one or few tokens.
 template <typename T, int NKB>
 int run(DeltaArgs a, hipStream_t s) {
+    const int nt = slice_tiles(a.seqs, a.Hv, a.Dv), slices = column_slices(a.Dv, nt);
+    int rc = 0;
+    a.shortest = a.seqs > 1 || a.tokens <= kShort ? kShort : -1;
+    if (a.shortest > 0) {
+        rc = by_tokens<T>(a, a.tokens <= kShort ? 0 : slices, s);
+        if (rc != 0 || a.tokens <= kShort) return rc;
+    }
     delta_prep_kernel<T, NKB><<<(int)a.places * a.Hk, 256, 0, s>>>(a);
-    int rc = (int)hipGetLastError();
-    if (rc != 0) return rc;
-    const int slices = column_slices(a.Dv, 1);
-    delta_chunks_kernel<T, NKB, 1><<<(a.seqs * a.Hv + 7) / 8 * 8 * slices, 256, 0, s>>>(a, slices);
     rc = (int)hipGetLastError();
+    if (rc != 0) return rc;
+    rc = nt == 2 ? chunks<T, NKB, 2>(a, slices, s) : chunks<T, NKB, 1>(a, slices, s);
     if (rc != 0 || !a.norm || a.tokens == 0) return rc;
-    delta_norm_kernel<T><<<(int)(((long long)a.tokens * a.Hv + 3) / 4), 256, 0, s>>>(a, slices);
+    // as many lanes as a row has vectors, a power of two of them
+    constexpr int VE = Vec<T>::N;
+    int width = 1;
+    while (width < 64 && width * VE < a.Dv) width *= 2;
+    const int rows = 256 / width * kNormRows;
+    const int grid = (int)(((long long)a.tokens * a.Hv + rows - 1) / rows);
+    const bool wide = a.Dv % VE == 0 && rows16(a.y, a.ldy, sizeof(T)) && (!a.z || rows16(a.z, a.ldz, sizeof(T)));
+    if (wide)
+        delta_norm_kernel<T, true><<<grid, 256, 0, s>>>(a, slices, width);
+    else
+        delta_norm_kernel<T, false><<<grid, 256, 0, s>>>(a, slices, width);
     return (int)hipGetLastError();
 }
 
@@ -763,18 +1139,6 @@ int pick_channels(const DeltaArgs& a, hipStream_t s) {
     }
 }
 
-template <typename T>
-int step(const DeltaArgs& a, hipStream_t s) {
-    const int tx = (a.Dv + 3) / 4, groups = (a.Dk + 15) / 16;
-    const int threads = (tx * groups + 63) / 64 * 64;
-    const bool wide = a.Dv % 4 == 0 && ((uintptr_t)a.state & 15) == 0;
-    if (wide)
-        delta_step_kernel<T, true><<<a.seqs * a.Hv, threads, 0, s>>>(a, tx, groups);
-    else
-        delta_step_kernel<T, false><<<a.seqs * a.Hv, threads, 0, s>>>(a, tx, groups);
-    return (int)hipGetLastError();
-}
-
 }  // namespace
 
 long long delta_workspace_bytes(const fcm_delta_problem& p) {
@@ -786,8 +1150,8 @@ long long delta_workspace_bytes(const fcm_delta_problem& p) {
 
 long long delta_threads(const fcm_delta_problem& p) {
     const long long prep = chunk_places(p.tokens, p.seqs) * p.Hk * 256;
-    const long long chunks = ((long long)p.seqs * p.Hv + 7) / 8 * 8 * column_slices(p.Dv, 1) * 256;
-    const long long norm = ((long long)p.tokens * p.Hv + 3) / 4 * 256;
+    const long long chunks = ((long long)p.seqs * p.Hv + 7) / 8 * 8 * column_slices(p.Dv, 1) * 512;
+    const long long norm = (long long)p.tokens * p.Hv * 64 + 255;
     const long long token = (long long)p.seqs * p.Hv * 1024;
     long long most = prep > chunks ? prep : chunks;
     most = most > norm ? most : norm;
@@ -801,6 +1165,13 @@ int launch_delta_fwd(DeltaArgs a, int dtype, void* stream) {
     const int e = dtype == FCM_F32 ? 4 : 2;
     a.wide_q = a.Dk % (16 / e) == 0 && rows16(a.q, a.ldq, e);
     a.wide_k = a.Dk % (16 / e) == 0 && rows16(a.k, a.ldk, e);
+    auto pairs = [](const void* p, long long ld, int Dv, int size) {
+        return Dv % 2 == 0 && ld % 2 == 0 && ((uintptr_t)p & (2 * size - 1)) == 0;
+    };
+    a.wide_v = pairs(a.v, a.ldv, a.Dv, e);
+    a.wide_z = pairs(a.z, a.ldz, a.Dv, e);
+    a.wide_y = pairs(a.y, a.ldy, a.Dv, e);
+    a.wide_state = pairs(a.state, 0, a.Dv, 4);
     hipStream_t s = (hipStream_t)stream;
     if (dtype == FCM_F32) return pick_channels<float>(a, s);
     if (dtype == FCM_F16) return pick_channels<_Float16>(a, s);
@@ -809,9 +1180,9 @@ int launch_delta_fwd(DeltaArgs a, int dtype, void* stream) {
 
 int launch_delta_step(const DeltaArgs& a, int dtype, void* stream) {
     hipStream_t s = (hipStream_t)stream;
-    if (dtype == FCM_F32) return step<float>(a, s);
-    if (dtype == FCM_F16) return step<_Float16>(a, s);
-    return step<__bf16>(a, s);
+    if (dtype == FCM_F32) return by_tokens<float>(a, 0, s);
+    if (dtype == FCM_F16) return by_tokens<_Float16>(a, 0, s);
+    return by_tokens<__bf16>(a, 0, s);
 }
 
 }  // namespace fcm

@@ -72,7 +72,8 @@ struct DeltaArgs {
     // set by the launcher
     long long places;  // for chunks, in the workspace
     float* squares;
-    int wide_q, wide_k;
+    int wide_q, wide_k, wide_v, wide_z, wide_y, wide_state;  // alignment for vectors
+    int shortest;  // sequences of up to so many tokens are another kernel's
 };
 int launch_delta_fwd(DeltaArgs a, int dtype, void* stream);
 int launch_delta_step(const DeltaArgs& a, int dtype, void* stream);

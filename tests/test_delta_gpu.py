@@ -118,6 +118,25 @@ def test_prompts(dtype, lens, Hk, Hv, Dk, Dv, opts, pad):
     _check(got, pool, want, T, Hv, Dv, dtype)
 
 
+@pytest.mark.parametrize("dtype,Dk,Dv,opts,pad", [
+    ("bf16", 32, 32, {}, 0), ("f16", 128, 30, {"gate": False}, 2), ("f32", 64, 31, {"norm": False}, 0),
+    ("bf16", 136, 32, {"norm": False}, 1), ("f32", 20, 32, {}, 4)])
+def test_prompts_of_many_sequences(dtype, Dk, Dv, opts, pad):
+    # so many sequences and heads that a slice has two tiles of columns
+    opts, lens = dict(opts), ([1, 9, 66, 0, 17, 3, 30, 2] * 16)[:128]
+    T, B = sum(lens), len(lens)
+    c = _inputs(Dk + Dv, dtype, T, B, 2, 4, Dk, Dv, B)
+    if not opts.pop("norm", True):
+        c["norm"] = None
+    if not opts.pop("gate", True):
+        c["z"] = None
+    slot_of, carry = [B - 1 - i for i in range(B)], [i % 3 for i in range(B)]
+    got, pool, spans = _call(c, dtype, lens, slot_of, carry, 2, 4, Dk, Dv, opts, pad)
+    want = delta(dtype, c["q"], c["k"], c["v"], c["a"], c["b"], c["A"], c["dt_bias"], c["norm"], c["z"], spans, slot_of,
+                 carry, c["state"], Dk ** -0.5, 1e-6)
+    _check(got, pool, want, T, 4, Dv, dtype)
+
+
 @pytest.mark.parametrize("dtype,Hk,Hv,Dk,Dv,opts", [
     ("bf16", 2, 4, 128, 128, {}), ("f16", 1, 2, 64, 128, {"norm": False}), ("f32", 1, 1, 256, 256, {}),
     ("bf16", 1, 3, 128, 64, {"gate": False}), ("f32", 2, 2, 72, 100, {"qk_norm": False}), ("f16", 1, 1, 1, 1, {"norm": False}),

@@ -30,7 +30,7 @@ def _delta(names, change):
     ({"scale": math.nan}, 1, "scale"), ({"dtype": 3}, 2, "int8"), ({"dtype": 9}, 1, "fcm_dtype"), ({"tokens": -1}, 1, "negative"),
     ({"seqs": -1}, 1, "negative"), ({"slots": None, "seqs": 3}, 1, "at least seqs slots"), ({"ldq": 127}, 1, "stride"),
     ({"ldk": 1}, 1, "stride"), ({"ldv": 127}, 1, "stride"), ({"lda": 3}, 1, "stride"), ({"ldb": 3}, 1, "stride"),
-    ({"ldz": 100}, 1, "stride"), ({"ldy": -128}, 1, "stride"), ({"ldy": (1 << 40) + 1}, 1, "2^40"),
+    ({"ldz": 100}, 1, "stride"), ({"ldy": -128}, 1, "stride"), ({"ldy": (1 << 40) + 1}, 1, "2^40"), ({"ldy": 1 << 22}, 2, "2^22"), ({"ldv": 1 << 30}, 2, "2^22"),
     ({"tokens": (1 << 31) - 1}, 1, "2^30"), ({"tokens": 1 << 29, "Hv": 1 << 14}, 2, "one launch"),
     ({"seqs": 1 << 24, "slots": 1 << 24}, 2, "one launch")])
 def test_delta_refusals(change, status, word):
