@@ -145,8 +145,49 @@ constexpr int kStep = 128;  // channels a wave takes at a time: 64 bytes of an o
 // step's own offset of up to 2^21 still below 2^32.
 constexpr uint32_t kBehind = 0xfc000000u;
 
-// A workgroup has 16 * RT output channels and 16 * MT tokens (or 4, 8: NI = 1, 2); its waves take
-// every NW-th step of 128 channels and add their sums through LDS.
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+
+// The scales of TILES tiles of 16 rows, kSteps steps of four blocks at a time, in the wave's own LDS: four lanes load 32
+// bytes of a row (a byte a step for itself would bring in the whole cache line each time).  Where a row has fewer than eight
+// left they are its last eight, moved down; a row of fewer than eight in all is loaded by bytes.
+constexpr int kSteps = 8;
+template <int TILES>
+struct StepScales {
+    const uint8_t* row[TILES];  // this lane's row of each tile, from the lane's eight blocks on
+    int blocks, part;
+    u32x2 raw[TILES];
+    __device__ __forceinline__ void fetch(int s0) {
+        const int want = 4 * s0 + part, at = want + 8 <= blocks ? want : blocks - 8;
+        if (blocks >= 8) {
+#pragma unroll
+            for (int r = 0; r < TILES; ++r) raw[r] = *(const u32x2_any*)(row[r] + at);
+        } else {
+#pragma unroll
+            for (int r = 0; r < TILES; ++r) {
+                raw[r] = u32x2{0, 0};
+                for (int b = want; b < blocks; ++b) raw[r][(b - want) >> 2] |= (uint32_t)row[r][b] << (8 * (b & 3));
+            }
+        }
+    }
+    __device__ __forceinline__ void stage(int s0, u32x2 (*to)[64]) const {
+        const int want = 4 * s0 + part;
+        int gone = blocks < 8 || want + 8 <= blocks ? 0 : want - (blocks - 8);
+        gone = gone < 8 ? gone : 8;
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) {
+            const uint64_t u = (__builtin_bit_cast(uint64_t, raw[r]) >> (4 * gone)) >> (4 * gone);
+            to[r][threadIdx.x & 63] = __builtin_bit_cast(u32x2, u);
+        }
+    }
+    // of row l % 16, block l / 16 of step j
+    __device__ __forceinline__ static uint32_t read(const u32x2* from, int j) {
+        const int lane = threadIdx.x & 63;
+        return ((const uint8_t*)from)[32 * (lane & 15) + 4 * j + (lane >> 4)];
+    }
+};
+
+// A workgroup has 16 * RT output channels and 16 * MT tokens (or 4, 8: NI = 1, 2); its waves share
+// the steps of 128 channels and add their sums through LDS.
 //
 // Four neighbouring lanes load 64 bytes of an output channel (16 lanes 256 bytes of a token), and the wave passes
 // them through its own piece of LDS, in 16-byte chunks whose place is turned by the row so that a column of them
@@ -159,6 +200,7 @@ __global__ __launch_bounds__(64 * NW) void mx4_kernel(Mx4Args a) {
     constexpr int XI = MT * NI, TOKENS = 4 * XI, XP = XPieces<T>::N;
     static_assert(TOKENS <= 32, "kBehind lies behind a tile's tokens");
     __shared__ u32x4 stage[NW][RT + XP * XI][64];
+    __shared__ u32x2 scales[NW][RT][64];
     auto part = [&](int w, int r, int i) { return (float*)stage[w] + (r * XI + i) * 64; };
     static_assert(RT * XI <= 4 * (RT + XP * XI), "the sums fit");
     const int lane = threadIdx.x & 63;
@@ -172,7 +214,6 @@ __global__ __launch_bounds__(64 * NW) void mx4_kernel(Mx4Args a) {
     const int trows = a.M - m0 < TOKENS ? a.M - m0 : TOKENS;
     const __amdgpu_buffer_rsrc_t rq =
         mm::rsrc(a.q + (long long)k0 * (a.C / 2), (uint32_t)krows * (a.C / 2));
-    const __amdgpu_buffer_rsrc_t rs = mm::rsrc(a.scales + (long long)k0 * blocks, (uint32_t)krows * blocks);
     const __amdgpu_buffer_rsrc_t rx = mm::rsrc((const T*)a.x + (long long)m0 * a.ldx,
                                                ((uint32_t)(trows - 1) * (uint32_t)a.ldx + a.C) * 2);
     uint32_t xat[XI];
@@ -183,17 +224,14 @@ __global__ __launch_bounds__(64 * NW) void mx4_kernel(Mx4Args a) {
     }
     struct Step {
         u32x4 w[RT], x[XI];
-        uint32_t scale[RT];
     };
     auto fetch = [&](int s, Step& v) {
         // (channels behind the last: codes and tokens read as zero)
-        const bool in = s * 4 + lchunk < blocks, mine = s * 4 + grp < blocks;
+        const bool in = s * 4 + lchunk < blocks;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const uint32_t at = (16 * r + lrow) * (uint32_t)(a.C / 2) + 16 * lchunk;
             v.w[r] = __builtin_amdgcn_raw_buffer_load_b128(rq, in ? at : mm::kOob, s * (kStep / 2), 0);
-            const uint32_t sat = (16 * r + sub) * (uint32_t)blocks + grp;
-            v.scale[r] = __builtin_amdgcn_raw_buffer_load_b8(rs, mine ? sat : mm::kOob, s * 4, 0);
         }
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
@@ -210,12 +248,12 @@ __global__ __launch_bounds__(64 * NW) void mx4_kernel(Mx4Args a) {
     // token of accumulator row `sub` (of 16 tokens)
     const int tok = (sub >> 2) * NI + ((sub & 3) < NI ? sub & 3 : 0);
     const int wplace = sub * 4 + (grp ^ (sub >> 2));
-    auto use = [&](Step& v, int then) {
+    auto use = [&](Step& v, int j, int then) {
         uint32_t scale[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             stage[wave][r][lane] = v.w[r];
-            scale[r] = v.scale[r];
+            scale[r] = StepScales<RT>::read(scales[wave][r], j);
         }
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
@@ -255,11 +293,29 @@ __global__ __launch_bounds__(64 * NW) void mx4_kernel(Mx4Args a) {
             }
         }
     };
-    const int last = steps - 1;
-    auto at_most = [&](int s) { return s < last ? s : last; };
-    Step v;
-    fetch(at_most(wave), v);
-    for (int s = wave; s < steps; s += NW) use(v, at_most(s + NW));
+    // each wave has neighbouring steps
+    const int share = (steps + NW - 1) / NW, first = wave * share, end = first + share < steps ? first + share : steps;
+    if (first < end) {
+        StepScales<RT> ss;
+        ss.blocks = blocks;
+        ss.part = 8 * (lane & 3);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            // (a row behind the last takes the last one's: it is not stored)
+            const int row = 16 * r + lrow < krows ? 16 * r + lrow : krows - 1;
+            ss.row[r] = a.scales + (long long)(k0 + row) * blocks;
+        }
+        Step v;
+        ss.fetch(first);
+        fetch(first, v);
+        for (int s0 = first; s0 < end; s0 += kSteps) {
+            ss.stage(s0, scales[wave]);
+            ss.fetch(s0 + kSteps < end ? s0 + kSteps : s0);
+            __builtin_amdgcn_wave_barrier();
+            const int n = end - s0 < kSteps ? end - s0 : kSteps;
+            for (int j = 0; j < n; ++j) use(v, j, s0 + j + 1 < end ? s0 + j + 1 : end - 1);
+        }
+    }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -291,6 +347,8 @@ int run(const Mx4Args& a, hipStream_t s) {
     };
     using std::integral_constant;
     const long long rows = (long long)((a.K + 15) / 16) * tiles;
+    if constexpr (NI == 4 && MT == 1)
+        if (rows >= 3000) return go(integral_constant<int, 4>(), integral_constant<int, 4>());
     if (rows >= 1024) return go(integral_constant<int, 2>(), integral_constant<int, 4>());
     return go(integral_constant<int, 1>(), integral_constant<int, 8>());
 }
@@ -307,7 +365,6 @@ int pick_tokens(const Mx4Args& a, hipStream_t s) {
 // tokens in 4 bits too
 // ------------------------------------------------------------------------------------------
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef u32x2 __attribute__((aligned(1))) u32x2_any;
 
 __device__ __forceinline__ i32x8 fp4_operand(u32x4 v) {
     return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
@@ -678,6 +735,7 @@ template <typename T, int MT, int RT, int NW>
 __global__ __launch_bounds__(64 * NW) void mx4x4_few_kernel(Mx4Args a) {
     constexpr int TILES = RT + MT;
     __shared__ u32x4 stage[NW][TILES > RT * MT ? TILES : RT * MT][64];
+    __shared__ u32x2 scales[NW][TILES][64];
     auto part = [&](int w, int r, int m) { return (f32x4*)stage[w] + (r * MT + m) * 64; };
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -690,20 +748,16 @@ __global__ __launch_bounds__(64 * NW) void mx4x4_few_kernel(Mx4Args a) {
     const uint32_t pitch = a.C / 2;
     const __amdgpu_buffer_rsrc_t rq = mm::rsrc(a.q + (long long)k0 * pitch, krows * pitch);
     const __amdgpu_buffer_rsrc_t rx = mm::rsrc((const uint8_t*)a.x + (long long)m0 * pitch, mrows * pitch);
-    const __amdgpu_buffer_rsrc_t rs = mm::rsrc(a.scales + (long long)k0 * blocks, (uint32_t)krows * blocks);
-    const __amdgpu_buffer_rsrc_t rt = mm::rsrc(a.xscales + (long long)m0 * blocks, (uint32_t)mrows * blocks);
     struct Step {
         u32x4 w[TILES];
-        uint32_t scale[TILES];
     };
     auto fetch = [&](int s, Step& v) {
-        const bool in = s * 4 + lchunk < blocks, mine = s * 4 + grp < blocks;
+        const bool in = s * 4 + lchunk < blocks;
 #pragma unroll
         for (int r = 0; r < TILES; ++r) {
             const int row = 16 * (r < RT ? r : r - RT);
-            const uint32_t at = (row + lrow) * pitch + 16 * lchunk, sat = (row + sub) * (uint32_t)blocks + grp;
+            const uint32_t at = (row + lrow) * pitch + 16 * lchunk;
             v.w[r] = __builtin_amdgcn_raw_buffer_load_b128(r < RT ? rq : rx, in ? at : mm::kOob, s * (kStep / 2), 0);
-            v.scale[r] = __builtin_amdgcn_raw_buffer_load_b8(r < RT ? rs : rt, mine ? sat : mm::kOob, s * 4, 0);
         }
     };
     f32x4 total[RT][MT];
@@ -712,28 +766,44 @@ __global__ __launch_bounds__(64 * NW) void mx4x4_few_kernel(Mx4Args a) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) total[r][m] = f32x4{};
     const int place = sub * 4 + (grp ^ (sub >> 2));
-    const int last = steps - 1;
-    auto at_most = [&](int s) { return s < last ? s : last; };
-    Step v;
-    fetch(at_most(wave), v);
-    for (int s = wave; s < steps; s += NW) {
-        uint32_t scale[TILES];
+    const int share = (steps + NW - 1) / NW, first = wave * share, end = first + share < steps ? first + share : steps;
+    if (first < end) {
+        StepScales<TILES> ss;
+        ss.blocks = blocks;
+        ss.part = 8 * (lane & 3);
 #pragma unroll
         for (int r = 0; r < TILES; ++r) {
-            stage[wave][r][lane] = v.w[r];
-            scale[r] = v.scale[r];
+            const int at = 16 * (r < RT ? r : r - RT) + lrow, most = (r < RT ? krows : mrows) - 1, row = at < most ? at : most;
+            ss.row[r] = r < RT ? a.scales + (long long)(k0 + row) * blocks : a.xscales + (long long)(m0 + row) * blocks;
         }
-        fetch(at_most(s + NW), v);
-        __builtin_amdgcn_wave_barrier();
-        i32x8 f[TILES];
+        Step v;
+        ss.fetch(first);
+        fetch(first, v);
+        for (int s0 = first; s0 < end; s0 += kSteps) {
+            ss.stage(s0, scales[wave]);
+            ss.fetch(s0 + kSteps < end ? s0 + kSteps : s0);
+            __builtin_amdgcn_wave_barrier();
+            const int n = end - s0 < kSteps ? end - s0 : kSteps;
+            for (int j = 0; j < n; ++j) {
+                uint32_t scale[TILES];
 #pragma unroll
-        for (int r = 0; r < TILES; ++r) f[r] = fp4_operand(stage[wave][r][place]);
-        __builtin_amdgcn_wave_barrier();
+                for (int r = 0; r < TILES; ++r) {
+                    stage[wave][r][lane] = v.w[r];
+                    scale[r] = StepScales<TILES>::read(scales[wave][r], j);
+                }
+                fetch(s0 + j + 1 < end ? s0 + j + 1 : end - 1, v);
+                __builtin_amdgcn_wave_barrier();
+                i32x8 f[TILES];
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+                for (int r = 0; r < TILES; ++r) f[r] = fp4_operand(stage[wave][r][place]);
+                __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-                total[r][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f[RT + m], f[r], total[r][m], 4, 4, 0, scale[RT + m], 0, scale[r]);
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        total[r][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f[RT + m], f[r], total[r][m], 4, 4, 0, scale[RT + m], 0, scale[r]);
+            }
+        }
     }
     __syncthreads();
 #pragma unroll
