@@ -1,6 +1,6 @@
-"""Convenience wrappers over the sequence operators: 4-bit pointwise layers, a state-space block
-with its carried states, and beam search.  Shapes, types and strides are checked here; the
-computation runs in the library's kernels.
+"""Convenience wrappers over the sequence operators: 4-bit pointwise layers, blocks with carried states
+(a selective scan or a gated delta rule), beam search, and the verification of drafted tokens.  Shapes,
+types and strides are checked here; the computation runs in the library's kernels.
 
 A block is  in-projection -> causal depthwise layer -> (step, B, C) projection -> selective scan
 gated by the in-projection's other half -> out-projection:
@@ -8,6 +8,15 @@ gated by the in-projection's other half -> out-projection:
     block = StateSpaceBlock(..., slots=16)
     y = block.prompt(x, cu, slots)        # packed prompts [tokens, dim]
     y = block.step(x, slots)              # one token of each sequence [batch, dim]
+
+(:class:`DeltaRuleBlock` has the same calls.)  Tokens that a smaller model has drafted are checked a
+whole row of them at a time, in slots of their own, and the states then moved on over those that stand:
+
+    verify = DraftVerifier(requests, drafts, vocab)
+    for p in pools: p[spare] = p[slots]          # int64 slots
+    logits = model(rows, cu, spare, carry)       # each request's last token and its drafts
+    accepted, following = verify(logits, tokens, draft_logits)
+    model(rows, *verify.kept(accepted, slots), carry)
 
 Every call works on torch's current stream.  With ``stream`` (a torch stream or a raw handle) all of
 it, the projections and what it allocates among it, works on that stream instead, behind what the
@@ -19,9 +28,11 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (ACT_CODES, beam_problem, dw1d_problem, fcm_beam_reorder, fcm_beam_select,
-               fcm_beam_workspace, fcm_dw1d_fwd, fcm_dw1d_step, fcm_q4_fwd, fcm_scan_fwd,
-               fcm_scan_step, fcm_scan_workspace, q4_problem, scan_problem)
+from . import (ACT_CODES, beam_problem, delta_problem, draft_problem, dw1d_problem, fcm_beam_reorder,
+               fcm_beam_select, fcm_beam_workspace, fcm_delta_fwd, fcm_delta_step, fcm_delta_workspace,
+               fcm_draft_verify, fcm_draft_workspace, fcm_dw1d_fwd, fcm_dw1d_step, fcm_mx4_dequantize,
+               fcm_mx4_fwd, fcm_mx4_quantize, fcm_mx4x4_fwd, fcm_q4_fwd, fcm_scan_fwd, fcm_scan_step,
+               fcm_scan_workspace, mx4_problem, q4_problem, scan_problem)
 
 DTYPE_NAMES = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
 
@@ -174,6 +185,85 @@ class Q4Linear:
         return out
 
 
+def quantize_mx4(x: torch.Tensor, stream=None):
+    """Codes [rows, C/2] and scales [rows, C/32], uint8, of [rows, C] values in blocks of 32 channels: a
+    power of two for the block, and for each channel the nearest of 0, 0.5, 1, 1.5, 2, 3, 4 and 6 with a
+    sign.  A value below the block's largest code is off by at most a quarter of itself or a quarter of
+    the scale, whichever is larger."""
+    if stream is not None:
+        return _on(stream, lambda: quantize_mx4(x), x)
+    _need(x.dtype in DTYPE_NAMES, "x must be float32, float16 or bfloat16")
+    _need(_on_gpu(x), "x must be on the current GPU")
+    _need(x.dim() == 2 and x.shape[1] > 0 and x.shape[1] % 32 == 0, "x must be [rows, C], C a multiple of 32")
+    rows, C = x.shape
+    x = _rows(x, C, x.dtype, "x", x.device)
+    q = torch.empty(rows, C // 2, dtype=torch.uint8, device=x.device)
+    scales = torch.empty(rows, C // 32, dtype=torch.uint8, device=x.device)
+    fcm_mx4_quantize(mx4_problem(DTYPE_NAMES[x.dtype], rows, C, 1, ldx=_stride(x)), x, q, scales)
+    return q, scales
+
+
+class MX4Linear:
+    """y = act(x W^T + bias) with W in microscaled 4-bit floating point: q [K, C/2] and scales [K, C/32],
+    uint8 (see :func:`quantize_mx4`), bias [K] float32 or None; activations of `dtype`.  With
+    `quantize_input` x goes into the same codes first and the product runs on the scaled matrix
+    instructions, for prompts of any length; without, it is meant for a few tokens."""
+
+    def __init__(self, q, scales, bias=None, act: str = "none", dtype: torch.dtype = torch.bfloat16,
+                 quantize_input: bool = False):
+        _need(q.dim() == 2 and q.dtype == torch.uint8 and q.is_contiguous() and q.shape[1] > 0 and
+              q.shape[1] % 16 == 0, "q must be [K, C/2] uint8, C a multiple of 32")
+        self.K, self.C = q.shape[0], q.shape[1] * 2
+        _need(scales.dtype == torch.uint8 and scales.is_contiguous() and
+              tuple(scales.shape) == (self.K, self.C // 32), f"scales must be [{self.K}, {self.C // 32}] uint8")
+        _need(bias is None or (bias.dtype == torch.float32 and tuple(bias.shape) == (self.K,) and
+                               bias.is_contiguous()), f"bias must be [{self.K}] float32")
+        for name, v in (("scales", scales), ("bias", bias)):
+            if v is not None:
+                _beside(v, q.device, name)
+        _need(act in ACT_CODES, f"act must be one of {sorted(ACT_CODES)}")
+        _need(dtype in (torch.float16, torch.bfloat16), "dtype must be float16 or bfloat16")
+        self.q, self.scales, self.bias = q, scales, bias
+        self.act, self.dtype, self.quantize_input = act, dtype, quantize_input
+
+    @classmethod
+    def from_weight(cls, weight, bias=None, act: str = "none", dtype: Optional[torch.dtype] = None,
+                    quantize_input: bool = False) -> "MX4Linear":
+        """Of a [K, C] weight on the GPU; dtype: the weight's if it is a 16-bit one, else bfloat16."""
+        if dtype is None:
+            dtype = weight.dtype if weight.dtype == torch.float16 else torch.bfloat16
+        return cls(*quantize_mx4(weight), bias=bias, act=act, dtype=dtype, quantize_input=quantize_input)
+
+    def weight(self) -> torch.Tensor:
+        """The [K, C] weight the codes stand for, in float32."""
+        _need(_on_gpu(self.q), "the weights must be on the current GPU")
+        w = torch.empty(self.K, self.C, device=self.q.device)
+        fcm_mx4_dequantize(mx4_problem("f32", self.K, self.C, 1), self.q, self.scales, w)
+        return w
+
+    def __call__(self, x, out=None, stream=None) -> torch.Tensor:
+        if stream is not None:
+            return _on(stream, lambda: self(x, out), x, out)
+        _need(_on_gpu(self.q), "the weights must be on the current GPU")
+        x = _rows(x, self.C, self.dtype, "x", self.q.device)
+        M = x.shape[0]
+        if out is None:
+            out = torch.empty(M, self.K, dtype=self.dtype, device=x.device)
+        else:
+            _out(out, M, self.K, self.dtype, x.device)
+        name = DTYPE_NAMES[self.dtype]
+        if self.quantize_input:
+            xq, xs = quantize_mx4(x)
+            fcm_mx4x4_fwd(mx4_problem(name, M, self.C, self.K, self.act, ldy=_stride(out)), xq, xs, self.q,
+                          self.scales, self.bias, out)
+            return out
+        if x.data_ptr() % 16 or _stride(x) % 8:
+            x = x.clone(memory_format=torch.contiguous_format)
+        fcm_mx4_fwd(mx4_problem(name, M, self.C, self.K, self.act, ldx=_stride(x), ldy=_stride(out)), x, self.q,
+                    self.scales, self.bias, out)
+        return out
+
+
 class StateSpaceBlock:
     """A state-space block and the states of `slots` sequences.  dim: the model's width, inner: the
     block's channels, N states of a channel, rank: width of the step's low-rank projection.
@@ -280,6 +370,93 @@ class StateSpaceBlock:
         return self.out_proj(y)
 
 
+class DeltaRuleBlock:
+    """A block of the gated delta rule and the states of `slots` sequences:  in-projection -> causal
+    depthwise layer with SiLU on queries, keys and values -> delta rule, its output normalised and gated
+    -> out-projection.  Hv value heads of Dv channels, Hk key heads of Dk (Hv a multiple of Hk).
+
+    in_proj: dim -> 2*Hk*Dk + 2*Hv*Dv + 2*Hv (queries, keys, values, gate, step, strength); conv_w
+    [2*Hk*Dk + Hv*Dv, W], conv_b the same in float32 or None; A [Hv] float32, negative; dt_bias [Hv]
+    float32 or None; norm [Dv] float32 or None; out_proj: Hv*Dv -> dim.  The projections are callables on
+    [rows, channels] such as :class:`MX4Linear`."""
+
+    def __init__(self, in_proj, conv_w, conv_b, A, dt_bias, norm, out_proj, Hk: int, Dk: int, Dv: int, slots: int,
+                 scale: float = 0.0, eps: float = 1e-6):
+        self.Hk, self.Hv, self.Dk, self.Dv = Hk, A.shape[0], Dk, Dv
+        self.keys, self.inner = Hk * Dk, A.shape[0] * Dv
+        self.mixed = 2 * self.keys + self.inner
+        _need(conv_w.dtype in DTYPE_NAMES, "conv_w must be float32, float16 or bfloat16")
+        _need(conv_w.dim() == 2 and conv_w.shape[0] == self.mixed, f"conv_w must be [{self.mixed}, W]")
+        _need(Hk > 0 and self.Hv % Hk == 0, "the value heads must be a multiple of the key heads")
+        for name, v, n in (("A", A, self.Hv), ("conv_b", conv_b, self.mixed), ("dt_bias", dt_bias, self.Hv),
+                           ("norm", norm, Dv)):
+            if v is not None:
+                _need(tuple(v.shape) == (n,) and v.dtype == torch.float32 and v.is_contiguous(),
+                      f"{name} must be [{n}] float32")
+                _beside(v, conv_w.device, name)
+        self.in_proj, self.out_proj = in_proj, out_proj
+        self.conv_w, self.conv_b, self.A, self.dt_bias, self.norm = conv_w.contiguous(), conv_b, A, dt_bias, norm
+        self.W, self.slots, self.scale, self.eps = conv_w.shape[1], slots, scale, eps
+        self.dtype, self.name = conv_w.dtype, DTYPE_NAMES[conv_w.dtype]
+        self.window = torch.zeros(slots, self.W - 1, self.mixed, dtype=self.dtype, device=conv_w.device)
+        self.state = torch.zeros(slots, self.Hv, Dk, Dv, device=conv_w.device)
+
+    _projected = StateSpaceBlock._projected
+    _index = StateSpaceBlock._index
+
+    def _parts(self, x):
+        """(queries, keys and values together, gate, step, strength): the in-projection's parts."""
+        p = self._projected(self.in_proj(x), x.shape[0], self.mixed + self.inner + 2 * self.Hv, "in_proj's result")
+        at = self.mixed + self.inner
+        return p[:, :self.mixed], p[:, self.mixed:at], p[:, at:at + self.Hv], p[:, at + self.Hv:]
+
+    def _conv(self, xs, seqs: int):
+        return dw1d_problem(self.name, self.mixed, self.W, tokens=xs.shape[0], seqs=seqs, slots=self.slots,
+                            ldx=_stride(xs))
+
+    def _rule(self, u, z, a, b, seqs: int):
+        """The rule's problem and its inputs: u's parts, and those beside it."""
+        prob = delta_problem(self.name, self.Hk, self.Hv, self.Dk, self.Dv, tokens=u.shape[0], seqs=seqs,
+                             slots=self.slots, scale=self.scale, eps=self.eps, ldq=_stride(u), ldk=_stride(u),
+                             ldv=_stride(u), lda=_stride(a), ldb=_stride(b), ldz=_stride(z))
+        return prob, (u[:, :self.keys], u[:, self.keys:2 * self.keys], u[:, 2 * self.keys:], a, b, self.A,
+                      self.dt_bias, self.norm, z)
+
+    def prompt(self, x, cu, slots, carry=None, stream=None) -> torch.Tensor:
+        """x: [tokens, dim], sequence b in rows cu[b] .. cu[b+1]-1 and state slot slots[b]; with
+        carry[b] != 0 it continues from there."""
+        if stream is not None:
+            return _on(stream, lambda: self.prompt(x, cu, slots, carry), x, cu, slots, carry)
+        _need(_on_gpu(self.window), "the block must be on the current GPU")
+        T, B, dev = x.shape[0], slots.shape[0], self.window.device
+        self._index(cu, B + 1, "cu")
+        self._index(slots, B, "slots")
+        self._index(carry, B, "carry")
+        xs, z, a, b = self._parts(x)
+        u = torch.empty(T, self.mixed, dtype=self.dtype, device=dev)
+        fcm_dw1d_fwd(self._conv(xs, B), xs, self.conv_w, self.conv_b, cu, slots, carry, self.window, u)
+        prob, parts = self._rule(u, z, a, b, B)
+        y = torch.empty(T, self.inner, dtype=self.dtype, device=dev)
+        ws = torch.empty(max(16, fcm_delta_workspace(prob)), dtype=torch.uint8, device=dev)
+        fcm_delta_fwd(prob, *parts, cu, slots, carry, self.state, ws, y)
+        return self.out_proj(y)
+
+    def step(self, x, slots, stream=None) -> torch.Tensor:
+        """x: [batch, dim], one token of the sequence in slots[b] (outside [0, slots): an idle row)."""
+        if stream is not None:
+            return _on(stream, lambda: self.step(x, slots), x, slots)
+        _need(_on_gpu(self.window), "the block must be on the current GPU")
+        B, dev = x.shape[0], self.window.device
+        self._index(slots, B, "slots")
+        xs, z, a, b = self._parts(x)
+        u = torch.empty(B, self.mixed, dtype=self.dtype, device=dev)
+        fcm_dw1d_step(self._conv(xs, B), xs, self.conv_w, self.conv_b, slots, self.window, u)
+        prob, parts = self._rule(u, z, a, b, B)
+        y = torch.empty(B, self.inner, dtype=self.dtype, device=dev)
+        fcm_delta_step(prob, *parts, slots, self.state, y)
+        return self.out_proj(y)
+
+
 class BeamSearch:
     """Beams of `requests` searches: their scores, done flags and state slots, moved on by each
     :meth:`advance`.  Beam i starts in state slot slots[i]; at first only the first beam of a request
@@ -337,3 +514,65 @@ class BeamSearch:
         self._next = (self.scores, self.done, self.slots)
         self.scores, self.done, self.slots = scores, done, slots
         return self.parent, self.token
+
+
+class DraftVerifier:
+    """Verification of up to `drafts` drafted tokens of each of `requests` requests: tokens drawn this way
+    are distributed as the target model's alone.  temperature 0: the largest logit alone counts."""
+
+    def __init__(self, requests: int, drafts: int, vocab: int, temperature: float = 1.0):
+        _need(requests >= 0 and drafts >= 1 and vocab >= 1, "sizes must be positive")
+        self.requests, self.drafts, self.vocab, self.temperature = requests, drafts, vocab, temperature
+
+    def _ints(self, t, n: int, name: str, device):
+        _beside(t, device, name)
+        _need(t.dtype == torch.int32 and t.numel() == n and t.is_contiguous(), f"{name} must have {n} int32 values")
+
+    def __call__(self, target, tokens, draft=None, counts=None, uniform=None, stream=None):
+        """target: logits [requests*(drafts+1), vocab] of the target model after a request's last token and
+        after each of its drafts; tokens: [requests, drafts] int32; draft: logits [requests*drafts, vocab]
+        that the tokens were drawn from (None: they were picked, with probability 1); counts: [requests]
+        int32, how many of its tokens a request uses (None: all); uniform: [requests*(drafts+1)] float32 in
+        [0, 1) (None: drawn here).  Returns (accepted, following), [requests] int32: how many tokens stand and
+        the one behind them, -1 behind a row without any finite logit."""
+        if stream is not None:
+            return _on(stream, lambda: self(target, tokens, draft, counts, uniform), target, tokens, draft, counts,
+                       uniform)
+        R, D, V = self.requests, self.drafts, self.vocab
+        _need(target.dtype in DTYPE_NAMES, "target must be float32, float16 or bfloat16")
+        _need(_on_gpu(target), "target must be on the current GPU")
+        dev = target.device
+        target = _rows(target, V, target.dtype, "target", dev)
+        _need(target.shape[0] == R * (D + 1), f"target must have {R * (D + 1)} rows")
+        if draft is not None:
+            draft = _rows(draft, V, target.dtype, "draft", dev)
+            _need(draft.shape[0] == R * D, f"draft must have {R * D} rows")
+        self._ints(tokens, R * D, "tokens", dev)
+        if counts is not None:
+            self._ints(counts, R, "counts", dev)
+        if uniform is None and self.temperature != 0:
+            uniform = torch.rand(R * (D + 1), device=dev)
+        if uniform is not None:
+            _beside(uniform, dev, "uniform")
+            _need(uniform.dtype == torch.float32 and uniform.numel() == R * (D + 1) and uniform.is_contiguous(),
+                  f"uniform must have {R * (D + 1)} float32 values")
+        prob = draft_problem(DTYPE_NAMES[target.dtype], R, D, V, self.temperature, ldt=_stride(target),
+                             ldd=0 if draft is None else _stride(draft))
+        ws = torch.empty(max(16, fcm_draft_workspace(prob)), dtype=torch.uint8, device=dev)
+        accepted = torch.empty(R, dtype=torch.int32, device=dev)
+        following = torch.empty(R, dtype=torch.int32, device=dev)
+        fcm_draft_verify(prob, target, draft, tokens, counts, uniform, ws, accepted, following)
+        return accepted, following
+
+    def kept(self, accepted, slots):
+        """(cu, slots) of 2*requests sequences for a block's ``prompt`` over the verified rows, each request's
+        last token and its drafts: the rows that stand move the state in the request's slot on, the rows
+        behind them belong to no slot.  (A caller's carry has 2*requests values.)"""
+        R, D = self.requests, self.drafts
+        self._ints(accepted, R, "accepted", accepted.device)
+        self._ints(slots, R, "slots", accepted.device)
+        first = torch.arange(0, R * (D + 1), D + 1, dtype=torch.int32, device=accepted.device)
+        cu = torch.empty(2 * R + 1, dtype=torch.int32, device=accepted.device)
+        cu[0:-1:2], cu[1::2] = first, first + accepted + 1
+        cu[-1:].fill_(R * (D + 1))
+        return cu, torch.stack([slots, torch.full_like(slots, -1)], 1).reshape(-1)
