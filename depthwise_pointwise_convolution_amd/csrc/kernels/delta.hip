@@ -507,11 +507,12 @@ __device__ __forceinline__ float sum16(float v) {
 }
 
 // The i-th sequence of more than `shortest` tokens, or -1.
-__device__ __forceinline__ int long_sequence(const int32_t* cu, int seqs, int shortest, int i) {
+__device__ __forceinline__ int long_sequence(const int32_t* cu, int seqs, int tokens, int shortest, int i) {
     if (shortest < 0) return i;
     const int lane = threadIdx.x & 63;
     for (int b = 0; b < seqs; b += 64) {
-        const bool in = b + lane < seqs && cu[b + lane + 1] - cu[b + lane] > shortest;
+        const bool in = b + lane < seqs &&
+                        seq_offset(cu, b + lane + 1, tokens) - seq_offset(cu, b + lane, tokens) > shortest;
         uint64_t who = __ballot(in);
         const int n = __popcll(who);
         if (i < n) {
@@ -547,7 +548,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slic
     // the slices of a head, which read the same operands, go to one XCD
     const int xcd = blockIdx.x & 7, rest = blockIdx.x >> 3;
     const int slice = rest % slices, bh = (rest / slices) * 8 + xcd;
-    const int b = bh < a.seqs * a.Hv ? long_sequence(a.cu, a.seqs, a.shortest, bh / a.Hv) : -1;
+    const int b = bh < a.seqs * a.Hv ? long_sequence(a.cu, a.seqs, a.tokens, a.shortest, bh / a.Hv) : -1;
     if (b < 0) return;
     const int h = bh % a.Hv, hk = h / (a.Hv / a.Hk);
     const int start = seq_offset(a.cu, b, a.tokens), end = seq_offset(a.cu, b + 1, a.tokens);
@@ -653,7 +654,6 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slic
         return;
     }
 
-    __builtin_amdgcn_s_setprio(2);  // the chain before the outputs
     const int slot = a.state ? seq_slot(a.slots, b, a.nslots) : -1;
     float* state = slot >= 0 ? a.state + ((long long)slot * a.Hv + h) * a.Dk * a.Dv : nullptr;
     const bool carried = state && a.carry && a.carry[b] != 0;

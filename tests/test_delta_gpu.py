@@ -274,3 +274,62 @@ def test_captured():
         torch.cuda.synchronize()
         for got, x in zip((y, y1, d["state"]), w):
             assert torch.equal(got, x)
+
+
+@pytest.mark.parametrize("cu", [[0, 30, 75], [0, 10, 75], [-9, 30, 2 ** 31 - 1], [-2 ** 31, 10, 99]])
+def test_offsets_beyond_the_rows_are_cut(cu):
+    # bit for bit what the offsets cut to 0 .. 50 give: which sequences are short goes by those too
+    import depthwise_pointwise_convolution_amd as F
+    T, B, Hk, Hv, Dk, Dv = 50, 2, 1, 2, 64, 32
+    c = _inputs(31, "bf16", T, B, Hk, Hv, Dk, Dv, B)
+    got = []
+    for offsets in (cu, [min(max(v, 0), T) for v in cu]):
+        d = {n: t.cuda() for n, t in c.items()}
+        y = torch.full((T, Hv, Dv), 7.0, dtype=torch.bfloat16, device="cuda")
+        p = F.delta_problem("bf16", Hk, Hv, Dk, Dv, tokens=T, seqs=B, slots=B)
+        ws = torch.full((F.fcm_delta_workspace(p),), 255, dtype=torch.uint8, device="cuda")
+        F.fcm_delta_fwd(p, d["q"], d["k"], d["v"], d["a"], d["b"], d["A"], d["dt_bias"], d["norm"], d["z"],
+                        torch.tensor(offsets, dtype=torch.int32).cuda(), None, torch.ones(B, dtype=torch.int32).cuda(),
+                        d["state"], ws, y)
+        torch.cuda.synchronize()
+        got.append((y.cpu(), d["state"].cpu()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert torch.isfinite(got[0][0].float()).all()
+
+
+@pytest.mark.parametrize("step", [True, False])
+def test_rows_and_states_far_apart(step):
+    # rows 2^30 elements apart, states behind the 2^31st element: bit for bit what dense ones give
+    import depthwise_pointwise_convolution_amd as F
+    T, Hk, Hv, Dk, Dv, far = 4 if step else 20, 1, 2, 128, 128, 2 ** 30 if step else 2 ** 28
+    slots = 2 ** 31 // (Hv * Dk * Dv) + 2
+    c = _inputs(32, "bf16", T, 1, Hk, Hv, Dk, Dv, T)
+    pool = torch.empty(slots, Hv, Dk, Dv, device="cuda")
+    got = []
+    for apart in (False, True):
+        d = {n: t.cuda().reshape(t.shape[0], -1) if n in "qkvabz" else t.cuda() for n, t in c.items()}
+        ld, state = {}, d["state"]
+        which = torch.arange(T if step else 1, dtype=torch.int32)
+        if apart:
+            wide = torch.empty((T - 1) * far + 1024, dtype=torch.bfloat16, device="cuda")
+            at = 0
+            for n in "qkab" + ("vz" if step else ""):
+                w = d[n].shape[1]
+                rows = wide.as_strided((T, w), (far, 1), at)
+                rows.copy_(d[n])
+                d[n], ld["ld" + n], at = rows, far, at + w
+            which = slots - 1 - which
+            pool[which.long().cuda()] = state[:len(which)]
+            state = pool
+        y = torch.empty(T, Hv * Dv, dtype=torch.bfloat16, device="cuda")
+        p = F.delta_problem("bf16", Hk, Hv, Dk, Dv, tokens=T, seqs=T if step else 1, slots=state.shape[0], **ld)
+        args = [d[n] for n in ("q", "k", "v", "a", "b", "A", "dt_bias", "norm", "z")]
+        if step:
+            F.fcm_delta_step(p, *args, which.cuda(), state, y)
+        else:
+            ws = torch.empty(F.fcm_delta_workspace(p), dtype=torch.uint8, device="cuda")
+            F.fcm_delta_fwd(p, *args, torch.tensor([0, T], dtype=torch.int32).cuda(), which.cuda(),
+                            torch.ones(1, dtype=torch.int32).cuda(), state, ws, y)
+        torch.cuda.synchronize()
+        got.append((y.cpu(), state[which.long().cuda()].cpu()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])

@@ -155,3 +155,36 @@ def test_captured():
         graph.replay()
         torch.cuda.synchronize()
         _compare(list(zip(*out.tolist())), target, draft, tokens, None, uniform, 1.0)
+
+
+@pytest.mark.parametrize("heat", [1.0, 0.0])
+def test_rows_far_apart(heat):
+    # rows 2^30 elements apart: what dense ones give
+    import depthwise_pointwise_convolution_amd as F
+    B, N, V, far = 2, 2, 1000, 2 ** 30
+    target, draft, tokens, uniform = _inputs(12, "bf16", B, N, V, heat)
+    wide = torch.empty((B * (N + 1) - 1) * far + 2 * V, dtype=torch.bfloat16, device="cuda")
+    t, d = wide.as_strided((B * (N + 1), V), (far, 1)), wide.as_strided((B * N, V), (far, 1), V)
+    t.copy_(target.reshape(-1, V))
+    d.copy_(draft.reshape(-1, V))
+    p = F.draft_problem("bf16", B, N, V, temperature=heat, ldt=far, ldd=far)
+    ws = torch.empty(F.fcm_draft_workspace(p), dtype=torch.uint8, device="cuda")
+    out = torch.zeros(2, B, dtype=torch.int32, device="cuda")
+    F.fcm_draft_verify(p, t, d, tokens.to(torch.int32).cuda(), None, uniform.cuda(), ws, out[0], out[1])
+    torch.cuda.synchronize()
+    _compare(list(zip(*out.tolist())), target, draft, tokens, None, uniform, heat)
+
+
+def test_two_at_once():
+    # two calls on streams of their own, each with its workspace
+    import depthwise_pointwise_convolution_amd.sequence as S
+    B, N, V = 6, 4, 20000
+    cases = [_inputs(seed, "bf16", B, N, V, 1.0) for seed in (21, 22)]
+    on = [tuple(c.cuda() for c in (t.reshape(-1, V), x.to(torch.int32), d.reshape(-1, V), u)) for t, d, x, u in cases]
+    verify = S.DraftVerifier(B, N, V)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [verify(t, x, d, uniform=u, stream=s) for (t, x, d, u), s in zip(on, streams)]
+    torch.cuda.synchronize()
+    for (a, n), (target, draft, tokens, uniform) in zip(got, cases):
+        _compare(list(zip(a.tolist(), n.tolist())), target, draft, tokens, None, uniform, 1.0)

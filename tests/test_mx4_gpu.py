@@ -193,3 +193,93 @@ def test_a_bad_token_stays_in_its_row():
     torch.cuda.synchronize()
     rest = [i for i in range(20) if i != 7]
     assert torch.equal(y[rest], z[rest]) and torch.isnan(z[7]).all()
+
+
+@pytest.mark.parametrize("both", [False, True])
+@pytest.mark.parametrize("M,C,K", [(1, 96, 48100), (7, 288, 48100), (16, 64, 50001), (17, 96, 48100), (40, 64, 48100)])
+def test_products_with_many_outputs(both, M, C, K):
+    import depthwise_pointwise_convolution_amd as F
+    g = torch.Generator().manual_seed(M + C + K)
+    codes, scales = _weights(K, C, M + C, 8)
+    xcodes, xscales = _weights(M, C, M + C + 1, 4)
+    x = mx4_values(xcodes, xscales)
+    bias = torch.randn(K, generator=g)
+    y = torch.full((M, K + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    p = F.mx4_problem("bf16", M, C, K, ldy=K + 3)
+    w, ws = mx4_pack(codes).cuda(), scales.to(torch.uint8).cuda()
+    if both:
+        F.fcm_mx4x4_fwd(p, mx4_pack(xcodes).cuda(), xscales.to(torch.uint8).cuda(), w, ws, bias.cuda(), y)
+    else:  # (a code's value has two bits: it is its own rounding)
+        F.fcm_mx4_fwd(p, x.to(torch.bfloat16).cuda(), w, ws, bias.cuda(), y)
+    torch.cuda.synchronize()
+    want, tol = product("bf16", x, mx4_values(codes, scales), bias, "none")
+    _within(y[:, :K], want, tol, "bf16")
+    assert (y[:, K:] == 7.0).all()
+
+
+def test_codes_behind_2_to_the_31st_byte():
+    # the last rows' codes, values and products are those of the rows alone
+    import depthwise_pointwise_convolution_amd as F
+    C, K, M, last = 2 ** 16, 2 ** 16 + 32, 3, 48
+    q = torch.randint(0, 256, (K, C // 2), dtype=torch.uint8, device="cuda")
+    s = torch.randint(120, 124, (K, C // 32), dtype=torch.uint8, device="cuda")
+    x = torch.randn(M, C, device="cuda").to(torch.bfloat16)
+    xq, xs = _quantise(x, "bf16")
+    tail = {}
+    for name, call in {
+            "16-bit": lambda k, w, t, y: F.fcm_mx4_fwd(F.mx4_problem("bf16", M, C, k), x, w, t, None, y),
+            "4-bit": lambda k, w, t, y: F.fcm_mx4x4_fwd(F.mx4_problem("bf16", M, C, k), xq, xs, w, t, None, y)}.items():
+        y = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+        call(K, q, s, y)
+        want = torch.empty(M, last, dtype=torch.bfloat16, device="cuda")
+        call(last, q[-last:].contiguous(), s[-last:].contiguous(), want)
+        torch.cuda.synchronize()
+        # (fewer outputs may be summed in another order: C products of either sign, each sum off by a rounding)
+        w = torch.empty(last, C, device="cuda")
+        F.fcm_mx4_dequantize(F.mx4_problem("f32", last, C), q[-last:].contiguous(), s[-last:].contiguous(), w)
+        v = torch.empty(M, C, device="cuda")
+        F.fcm_mx4_dequantize(F.mx4_problem("f32", M, C), xq, xs, v)
+        right, tol = product("bf16", (v if name == "4-bit" else x).cpu(), w.cpu().double(), None, "none")
+        _within(y[:, -last:], right, tol, "bf16")
+        _within(want, right, tol, "bf16")
+        tail[name] = w
+    values = torch.empty(K, C, dtype=torch.bfloat16, device="cuda")
+    F.fcm_mx4_dequantize(F.mx4_problem("bf16", K, C), q, s, values)
+    assert torch.equal(values[-last:].float(), tail["4-bit"])
+    q2, s2 = torch.zeros_like(q), torch.zeros_like(s)
+    F.fcm_mx4_quantize(F.mx4_problem("bf16", K, C), values, q2, s2)
+    again = torch.empty(K, C, dtype=torch.bfloat16, device="cuda")
+    F.fcm_mx4_dequantize(F.mx4_problem("bf16", K, C), q2, s2, again)
+    torch.cuda.synchronize()
+    # (a block whose largest code is below 4 goes to a smaller scale, with the same values)
+    assert torch.equal(again[-last:], values[-last:]) and torch.equal(again[:last], values[:last])
+
+
+def test_captured():
+    import depthwise_pointwise_convolution_amd as F
+    M, C, K = 40, 256, 130
+    codes, scales = _weights(K, C, 3)
+    w, ws = mx4_pack(codes).cuda(), scales.to(torch.uint8).cuda()
+    x = torch.zeros(M, C, dtype=torch.bfloat16, device="cuda")
+    xq, xs = torch.empty(M, C // 2, dtype=torch.uint8, device="cuda"), torch.empty(M, C // 32, dtype=torch.uint8, device="cuda")
+    p = F.mx4_problem("bf16", M, C, K)
+
+    def run(y, z):
+        F.fcm_mx4_quantize(p, x, xq, xs)
+        F.fcm_mx4x4_fwd(p, xq, xs, w, ws, None, y)
+        F.fcm_mx4_fwd(p, x, w, ws, None, z)
+
+    y, z, y2, z2 = (torch.empty(M, K, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    run(y, z)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(y, z)
+    for seed in range(3):
+        x.copy_(torch.randn(M, C, generator=torch.Generator().manual_seed(seed)))
+        xq.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        run(y2, z2)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(z, z2)
