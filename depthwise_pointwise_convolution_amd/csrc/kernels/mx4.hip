@@ -346,10 +346,17 @@ int run(const Mx4Args& a, hipStream_t s) {
         return (int)hipGetLastError();
     };
     using std::integral_constant;
+    // Wide layers: more output channels a workgroup, which share the tokens' operands, on fewer waves, which join
+    // fewer sums; narrow ones need every wave there is.  At 4096 channels, us: 1 token, one tile on 8 waves / two on
+    // 4: 12288 outputs 6.9 / 7.1, 16384 10.4 / 8.9, 32768 18.6 / 16.3; 16 tokens, one on 8 / two / four on 4: 8192 7.3 / - / 7.8,
+    // 12288 11.6 / - / 8.6, 32768 30.7 / 22.1 / 18.8, 65536 58 / 52 / 40; 32 tokens, one on 8 / two on 4: 4096 6.3 / 7.7,
+    // 8192 10.2 / 8.4, 65536 85 / 53.
     const long long rows = (long long)((a.K + 15) / 16) * tiles;
-    if constexpr (NI == 4 && MT == 1)
-        if (rows >= 3000) return go(integral_constant<int, 4>(), integral_constant<int, 4>());
-    if (rows >= 1024) return go(integral_constant<int, 2>(), integral_constant<int, 4>());
+    if constexpr (NI == 4 && MT == 1) {
+        if (rows >= 768) return go(integral_constant<int, 4>(), integral_constant<int, 4>());
+    } else {
+        if (rows >= (MT == 2 ? 512 : 1024)) return go(integral_constant<int, 2>(), integral_constant<int, 4>());
+    }
     return go(integral_constant<int, 1>(), integral_constant<int, 8>());
 }
 
@@ -867,14 +874,24 @@ int product(const Mx4Args& a, hipStream_t s) {
     const integral_constant<int, 2> two;
     const integral_constant<int, 4> four;
     const integral_constant<int, 8> eight;
-    if (a.M <= 64) {
-        const long long rows = (a.K + 15) / 16;
-        if (a.M <= 16) return rows >= 1024 ? few(one, two, four) : few(one, one, eight);
-        if (a.M <= 32) return rows >= 1024 ? few(two, two, four) : few(two, one, eight);
-        return rows >= 1024 ? few(four, two, four) : few(four, one, eight);
+    // Few outputs leave tiles of 128 x 128 on few CUs, each with a long way over the channels to itself; many tokens have
+    // the waves that share the channels read the weights again for every 64 of them.  At 4096 channels, us, shared / tiles:
+    // 16 x 4096 outputs 4.5 / 22, 128 x 8192 11 / 22, 32 x 32768 22 / 28, 256 x 4096 11 / 22, 48 x 32768 31 / 29, 256 x 8192
+    // 23 / 22, 256 x 32768 84 / 38.  (Two output tiles on 4 waves or one on 8: 16 x 4096 5.4 / 4.5, 32 x 8192 6.4 / 7.5,
+    // 64 x 8192 8.1 / 11.)
+    if (a.M <= 32 || (long long)a.M * a.K <= 1 << 20) {
+        const int tokens = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64;
+        const bool wide = (long long)((a.K + 15) / 16) * ((a.M + tokens - 1) / tokens) >= 512;
+        if (tokens == 16) return wide ? few(one, two, four) : few(one, one, eight);
+        if (tokens == 32) return wide ? few(two, two, four) : few(two, one, eight);
+        return wide ? few(four, two, four) : few(four, one, eight);
     }
+    // Tiles of 256 x 256 take one CU each, and 41 us for 4096 channels whether they fill the card or not: 2048 x 4096
+    // outputs (128 tiles) take 33 us in those of 128 x 128, 2560 x 4096 43, 3328 x 4096 60 / 41, 8192 x 4096 115 / 86.
+    // Their longer start and end want channels to pay for them: 4096 x 4096 outputs of 256 channels 17 / 16 us, of 1024
+    // 22 / 22, of 4096 45 / 61.
     const int ktiles = (a.K + 255) / 256, mtiles = (a.M + 255) / 256;
-    if ((long long)ktiles * mtiles >= 192 && a.C >= 256) {
+    if ((long long)ktiles * mtiles >= 160 && a.C >= 1024) {
         mx4x4_large_kernel<T><<<ktiles * mtiles, 256, 0, s>>>(a, mtiles, ktiles);
         return (int)hipGetLastError();
     }

@@ -217,6 +217,21 @@ def test_products_with_many_outputs(both, M, C, K):
     assert (y[:, K:] == 7.0).all()
 
 
+@pytest.mark.parametrize("M,C,K", [(2500, 1056, 4100), (70, 96, 8200), (300, 1056, 3300), (250, 224, 4100), (65, 64, 16200)])
+def test_products_of_4_bit_tokens_by_size(M, C, K):
+    # each way the outputs are shared out
+    import depthwise_pointwise_convolution_amd as F
+    codes, scales = _weights(K, C, M + C, 8)
+    xcodes, xscales = _weights(M, C, M + C + 1, 8)
+    y = torch.full((M + 1, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    F.fcm_mx4x4_fwd(F.mx4_problem("bf16", M, C, K), mx4_pack(xcodes).cuda(), xscales.to(torch.uint8).cuda(),
+                    mx4_pack(codes).cuda(), scales.to(torch.uint8).cuda(), None, y)
+    torch.cuda.synchronize()
+    want, tol = product("bf16", mx4_values(xcodes, xscales), mx4_values(codes, scales), None, "none")
+    _within(y[:M], want, tol, "bf16")
+    assert (y[M] == 7.0).all()
+
+
 def test_codes_behind_2_to_the_31st_byte():
     # the last rows' codes, values and products are those of the rows alone
     import depthwise_pointwise_convolution_amd as F
