@@ -580,7 +580,7 @@ fcm_status fcm_mx4_dequantize(const fcm_mx4_problem* prob, const void* q, const 
 
 /* Pointwise layer y[m][k] = act(bias[k] + sum_c W[k][c] * x[m][c]) with W in codes: q [K][C/2], scales
  * [K][C/32], bias [K] fp32 or NULL.  x: [M][C] in the storage type; for a few tokens (the weights are
- * read once for every 32 of them).  Products of a block's values are exact and summed in fp32.  x and q need
+ * read and converted once for every 32 of them).  Products of a block's values are exact and summed in fp32.  x and q need
  * 16-byte alignment and ldx a multiple of 8. */
 fcm_status fcm_mx4_fwd(const fcm_mx4_problem* prob, const void* x, const void* q, const uint8_t* scales,
                        const float* bias, void* y, void* stream);
