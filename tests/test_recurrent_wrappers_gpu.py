@@ -182,3 +182,22 @@ def test_steps_and_verifications_in_a_graph():
         torch.cuda.synchronize()
         for i, (a, c) in enumerate(zip(out + [fresh.window, fresh.state], want[k])):
             assert torch.equal(a, c), (k, i)
+
+
+def test_nothing_to_do():
+    import depthwise_pointwise_convolution_amd.sequence as S
+    g = torch.Generator().manual_seed(8)
+    b, head, both = _block(S), _linear(S, g, 128, 70), _linear(S, g, 128, 70, quantize_input=True)
+    b.state.fill_(1.0)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    x = torch.zeros(0, 128, dtype=BF, device="cuda")
+    assert b.prompt(x, torch.zeros(1, dtype=torch.int32, device="cuda"), none).shape == (0, 128)
+    assert b.step(x, none).shape == (0, 128)
+    # (an empty prompt that carries nothing on starts its slot from zero, one that does leaves it)
+    zeros = torch.zeros(3, dtype=torch.int32, device="cuda")
+    b.prompt(x, zeros, torch.tensor([1, 4], dtype=torch.int32).cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda())
+    assert (b.state[1] == 0).all() and (b.state[[0, 2, 3, 4, 5]] == 1).all()
+    assert head(x).shape == (0, 70) and both(x).shape == (0, 70)
+    accepted, following = S.DraftVerifier(0, 4, 70)(head(x), none)
+    assert accepted.shape == following.shape == (0,)
+    assert S.quantize_mx4(x)[0].shape == (0, 64)
