@@ -163,15 +163,15 @@ __device__ __forceinline__ void st_operand(char* p, u32x4 v) {
 }
 
 // One workgroup per chunk and key head.  What is written bounds it: for 8192 tokens of 16 key heads and 32 value heads of
-// 128 channels 225 MB (and 100 MB read) in 97 us, 3.4 TB/s; half of the rest is the steps' latency, which four workgroups
-// a CU share.
+// 128 channels 225 MB (and 100 MB read) in 95 us, 3.4 TB/s; where there are few workgroups it is the latency of one, 26 us.
+// The value heads' decays are summed four heads at a time, a wave each, while the rows are under way.
 template <typename T, int NKB>
 __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
     constexpr int PI = Pieces<T>::IN, PQ = Pieces<T>::OUT, DK = 32 * NKB, LD = DK + 8, LM = 68;
     constexpr int kIn = 2 * kChunk * LD * (int)sizeof(T), kMat = 2 * kChunk * LM * 4;
     __shared__ __attribute__((aligned(16))) char smem[kIn > kMat ? kIn : kMat];
-    __shared__ double along[kChunk];
-    __shared__ float beta[kChunk], rq[kChunk], rk[kChunk];
+    __shared__ double alongs[4][kChunk];  // of four value heads, a wave each
+    __shared__ float betas[4][kChunk], rq[kChunk], rk[kChunk];
     T* in = (T*)smem;             // q rows, then k rows
     float* m1 = (float*)smem;     // (after their last use) output weights, then L
     float* m2 = m1 + kChunk * LM; // its inverse
@@ -195,6 +195,28 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
     char* key = (char*)a.ws + (place * a.Hk + hk) * lay.key_bytes;
     char* heads = (char*)a.ws + a.places * a.Hk * lay.key_bytes;
 
+    // decays from the chunk's start and rates of head h0 + wave
+    const int share = a.Hv / a.Hk;
+    T ga, gb;
+    auto load_steps = [&](int h0) {
+        const bool in = h0 + wave < (hk + 1) * share && lane < n;
+        ga = in ? ((const T*)a.a)[(t0 + lane) * a.lda + h0 + wave] : (T)0.0f;
+        gb = in ? ((const T*)a.b)[(t0 + lane) * a.ldb + h0 + wave] : (T)0.0f;
+    };
+    auto add_steps = [&](int h0) {
+        const int h = h0 + wave;
+        if (h >= (hk + 1) * share) return;
+        double p = lane < n ? log_decay(ga, a.dt_bias ? a.dt_bias[h] : 0.0f, a.A[h], a.softplus) : 0.0;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double v = __shfl_up(p, o);
+            if (lane >= o) p += v;
+        }
+        alongs[wave][lane] = p;
+        betas[wave][lane] = lane < n ? rate_of(gb) : 0.0f;
+    };
+    load_steps(hk * share);
+
     // rows into LDS, zero behind the sequence and behind the last channel
     constexpr int VE = Vec<T>::N;
 #pragma unroll
@@ -217,6 +239,7 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
             }
         }
     }
+    add_steps(hk * share);
     __syncthreads();
     // the rows' norms: four lanes a row
     {
@@ -287,26 +310,19 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
                 qk[j] = mm_pieces<PI, PI, PQ>(fq, fb, qk[j]);
             }
     }
-    const int share = a.Hv / a.Hk;
     for (int h = hk * share; h < (hk + 1) * share; ++h) {
         char* head = heads + (place * a.Hv + h) * lay.head_bytes;
+        const int hi = (h - hk * share) & 3;
         __syncthreads();  // (the rows in LDS, or the last head's matrices, are done with)
-        if (wave == 0) {
-            double p = 0.0;
-            float r = 0.0f;
-            if (lane < n) {
-                const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-                p = log_decay(((const T*)a.a)[(t0 + lane) * a.lda + h], bias, A, a.softplus);
-                r = rate_of(((const T*)a.b)[(t0 + lane) * a.ldb + h]);
-            }
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const double v = __shfl_up(p, o);
-                if (lane >= o) p += v;
-            }
-            along[lane] = p;
-            beta[lane] = r;
-            const double last = __shfl(p, 63);
+        if (hi == 0 && h > hk * share) {
+            load_steps(h);
+            add_steps(h);
+            __syncthreads();
+        }
+        const double* along = alongs[hi];
+        const float* beta = betas[hi];
+        if (wave == 1) {
+            const double p = along[lane], last = along[kChunk - 1];
             const float grown = __builtin_amdgcn_exp2f((float)p);
             float* rows = (float*)(head + lay.rows);
             rows[lane] = grown * rk[lane];
@@ -314,7 +330,6 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
             rows[2 * kChunk + lane] = __builtin_amdgcn_exp2f((float)(last - p)) * rk[lane];
             if (lane == 0) rows[3 * kChunk] = __builtin_amdgcn_exp2f((float)last);
         }
-        __syncthreads();
         f32x4 low[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)

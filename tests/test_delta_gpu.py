@@ -333,3 +333,14 @@ def test_rows_and_states_far_apart(step):
         torch.cuda.synchronize()
         got.append((y.cpu(), state[which.long().cuda()].cpu()))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 4), (2, 10), (1, 9)])
+def test_key_heads_shared_by_many(Hk, Hv):
+    lens, Dk, Dv = [70, 3, 40], 40, 24
+    T, B = sum(lens), len(lens)
+    c = _inputs(41 + Hv, "bf16", T, B, Hk, Hv, Dk, Dv, B)
+    got, pool, spans = _call(c, "bf16", lens, [2, 0, 1], [1, 0, 1], Hk, Hv, Dk, Dv, {})
+    want = delta("bf16", c["q"], c["k"], c["v"], c["a"], c["b"], c["A"], c["dt_bias"], c["norm"], c["z"], spans, [2, 0, 1],
+                 [1, 0, 1], c["state"], Dk ** -0.5, 1e-6)
+    _check(got, pool, want, T, Hv, Dv, "bf16")
