@@ -482,13 +482,14 @@ __global__ __launch_bounds__(64 * WK * WM, 2) void mx4x4_kernel(Mx4Args a, int m
     // Scales of kSpan steps at a time: a step loads some of the rows, 32 bytes of four lanes each, for the steps after the
     // present eight.  Where two steps have fewer than eight they are the last eight of the row, moved down on
     // their way to LDS.  (A row behind the last takes the last one's: its outputs are not stored.  Rows of fewer than
-    // eight are loaded before the first step, and here any eight bytes, which no step uses.)
+    // eight are loaded before the first step, and here any eight bytes, which no step uses: of the side's own codes,
+    // 16 bytes for each scale, so that they end before the last row of that side does.)
     constexpr int PARTS = ROWS / SROWS;
     u32x2 sraw;
     const int spart = tid & 3;
     const bool some = blocks >= 8;
     const uint8_t* kscales = some ? a.scales + (long long)k0 * blocks : a.q;
-    const uint8_t* mscales = some ? a.xscales + (long long)m0 * blocks : a.q;
+    const uint8_t* mscales = some ? a.xscales + (long long)m0 * blocks : (const uint8_t*)a.x;
     auto scale_at = [&](int group) {
         const int b = 4 * kSpan * group + 8 * spart;
         return b < blocks ? b : blocks & ~7;
