@@ -589,6 +589,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slic
     if (outputs) {
         const bool gate = !a.norm && a.z;
         const ChunkRows<T, NT> ys(a.y, a.ldy, hv, col, a.Dv, tok, a.wide_y), zs(a.z, a.ldz, hv, col, a.Dv, tok, a.wide_z);
+        const ChunkRows<float, NT> os(a.outs, (long long)a.Hv * a.Dv, hv, col, a.Dv, tok, a.Dv % 2 == 0);
         u32x4 q[NKB][PI], pw[2][PQ];
         f32x4 seen;
         T z[4][NT];
@@ -669,7 +670,10 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slic
                     for (int i = 0; i < 4; ++i)
                         if (t0 + tok + i < end) to[(long long)i * a.Hv * slices] = squares[i];
             }
-            ys.store(t0, end, o);
+            if (a.norm && sizeof(T) < 4)
+                os.store(t0, end, o);
+            else
+                ys.store(t0, end, o);
         }
         return;
     }
@@ -882,10 +886,12 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slic
             }
 }
 
-// The output's norm and gate, in place: the second kernel's slices left their sums of squares, a negative one the
-// short sequences' kernel, which has done it all.  A group of `width` lanes has kNormRows rows of heads, one after the
-// other in memory, whose loads are all under way before the first is used.  HBM bounds it: 8192 tokens of 32 heads of 128
-// channels, 201 MB, in 46 us, 4.4 TB/s.
+// The output's norm and gate: the second kernel left the outputs in 32 bits (in the workspace, or in y where that has
+// them) and its slices their sums of squares, a negative one the short sequences' kernel, which has done it all.  A group
+// of `width` lanes has kNormRows rows of heads, one after the other in memory, whose loads are all under way before the
+// first is used.  HBM bounds it: 8192 tokens of 32 heads of 128 channels in bf16, 268 MB, in 56 us, 4.8 TB/s.  z is read and
+// y written without a place in the caches, which leaves it to the outputs (with one: 61 us).  Outputs in the storage type would
+// be 67 MB less to read, but a second rounding, and infinite above fp16's largest number though the norm brings them to 1.
 constexpr int kNormRows = 4;
 template <typename T, bool WIDE>
 __global__ __launch_bounds__(256) void delta_norm_kernel(DeltaArgs a, int slices, int width) {
@@ -895,7 +901,8 @@ __global__ __launch_bounds__(256) void delta_norm_kernel(DeltaArgs a, int slices
     const uint32_t first = (uint32_t)blockIdx.x * (groups * kNormRows) + threadIdx.x / width;
     const int from = seq_offset(a.cu, 0, a.tokens), to = seq_offset(a.cu, a.seqs, a.tokens);
     T* y[kNormRows];
-    u32x4 vy[kNormRows], vz[kNormRows];
+    const float* o[kNormRows];
+    u32x4 vo[kNormRows][VE / 4], vz[kNormRows];
     float s[kNormRows], norm[VE];
     bool live[kNormRows];
     const int c = x * VE;  // (WIDE: a row has no more vectors than lanes)
@@ -907,9 +914,11 @@ __global__ __launch_bounds__(256) void delta_norm_kernel(DeltaArgs a, int slices
         live[r] = t >= from && t < to;
         if (!live[r]) continue;
         y[r] = (T*)a.y + t * a.ldy + (long long)h * a.Dv;
+        o[r] = sizeof(T) < 4 ? a.outs + (long long)id * a.Dv : (const float*)y[r];
         if (WIDE && c < a.Dv) {
-            vy[r] = ld16(y[r] + c);
-            if (a.z) vz[r] = ld16((const T*)a.z + t * a.ldz + (long long)h * a.Dv + c);
+#pragma unroll
+            for (int i = 0; i < VE / 4; ++i) vo[r][i] = ld16(o[r] + c + 4 * i);
+            if (a.z) vz[r] = __builtin_nontemporal_load((const u32x4*)((const T*)a.z + t * a.ldz + (long long)h * a.Dv + c));
         }
         s[r] = a.squares[(long long)id * slices];
         if (s[r] < 0.0f) live[r] = false;
@@ -925,21 +934,22 @@ __global__ __launch_bounds__(256) void delta_norm_kernel(DeltaArgs a, int slices
         if constexpr (WIDE) {
             if (c >= a.Dv) continue;
             float v[VE], g[VE];
-            unpack16<T>(vy[r], v);
+#pragma unroll
+            for (int i = 0; i < VE / 4; ++i) unpack16<float>(vo[r][i], v + 4 * i);
             if (a.z) unpack16<T>(vz[r], g);
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
                 v[i] *= f * norm[i];
                 if (a.z) v[i] *= silu(g[i]);
             }
-            st16(y[r] + c, pack16<T>(v));
+            __builtin_nontemporal_store(pack16<T>(v), (u32x4*)(y[r] + c));
         } else {
             const uint32_t id = first + r * groups;
             const long long t = id / (uint32_t)a.Hv;
             const int h = id - (uint32_t)t * a.Hv;
             const T* z = a.z ? (const T*)a.z + t * a.ldz + (long long)h * a.Dv : nullptr;
             for (int i = x; i < a.Dv; i += width) {
-                float v = (float)y[r][i] * f * a.norm[i];
+                float v = o[r][i] * f * a.norm[i];
                 if (z) v *= silu((float)z[i]);
                 y[r][i] = (T)v;
             }
@@ -1108,6 +1118,10 @@ long long chunk_places(int tokens, int seqs) { return (long long)tokens / kChunk
 // of four 172 / 159; 8192 tokens, 32 heads of eight 397 / 334.
 int slice_tiles(int seqs, int Hv, int Dv) { return (long long)seqs * Hv * ((Dv + 31) / 32) >= 512 ? 2 : 1; }
 int column_slices(int Dv, int nt) { return (Dv + 16 * nt - 1) / (16 * nt); }
+// 32-bit outputs before the norm (y holds those of 32-bit types)
+long long outs_bytes(int tokens, int Hv, int Dv, int dtype) {
+    return dtype == FCM_F32 ? 0 : ((long long)tokens * Hv * Dv * 4 + 15) / 16 * 16;
+}
 
 template <typename T, int NKB, int NT>
 int chunks(const DeltaArgs& a, int slices, hipStream_t s) {
@@ -1172,7 +1186,7 @@ int pick_channels(const DeltaArgs& a, hipStream_t s) {
 long long delta_workspace_bytes(const fcm_delta_problem& p) {
     const Layout l = layout(pieces_in(p.dtype), pieces_out(p.dtype), k_blocks(p.Dk));
     const long long places = chunk_places(p.tokens, p.seqs);
-    return places * (p.Hk * l.key_bytes + p.Hv * l.head_bytes) +
+    return places * (p.Hk * l.key_bytes + p.Hv * l.head_bytes) + outs_bytes(p.tokens, p.Hv, p.Dv, p.dtype) +
            (long long)p.tokens * p.Hv * column_slices(p.Dv, 1) * 4;
 }
 
@@ -1189,7 +1203,8 @@ long long delta_threads(const fcm_delta_problem& p) {
 int launch_delta_fwd(DeltaArgs a, int dtype, void* stream) {
     const Layout l = layout(pieces_in(dtype), pieces_out(dtype), k_blocks(a.Dk));
     a.places = chunk_places(a.tokens, a.seqs);
-    a.squares = (float*)((char*)a.ws + a.places * (a.Hk * l.key_bytes + a.Hv * l.head_bytes));
+    a.outs = (float*)((char*)a.ws + a.places * (a.Hk * l.key_bytes + a.Hv * l.head_bytes));
+    a.squares = (float*)((char*)a.outs + outs_bytes(a.tokens, a.Hv, a.Dv, dtype));
     const int e = dtype == FCM_F32 ? 4 : 2;
     a.wide_q = a.Dk % (16 / e) == 0 && rows16(a.q, a.ldq, e);
     a.wide_k = a.Dk % (16 / e) == 0 && rows16(a.k, a.ldk, e);

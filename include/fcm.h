@@ -522,7 +522,7 @@ int64_t fcm_delta_workspace(const fcm_delta_problem* prob);
 /* Prompts.  q, k: [tokens][Hk][Dk]; v, z, y: [tokens][Hv][Dv] (z may be NULL); a, b: [tokens][Hv];
  * A: [Hv] fp32; dt_bias: [Hv] fp32 or NULL; norm: [Dv] fp32 or NULL; state: [slots][Hv][Dk][Dv] fp32,
  * read where carry says so and always written (NULL as for fcm_dw1d_fwd); workspace as for
- * fcm_scan_fwd; ldv, ldz and ldy below 2^22.  With a norm, o is rounded to the storage type once before it (its squares are not). */
+ * fcm_scan_fwd; ldv, ldz and ldy below 2^22.  Only y is rounded to the storage type. */
 fcm_status fcm_delta_fwd(const fcm_delta_problem* prob, const void* q, const void* k, const void* v,
                          const void* a, const void* b, const float* A, const float* dt_bias,
                          const float* norm, const void* z, const int32_t* cu, const int32_t* slots,
