@@ -11,6 +11,7 @@ namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 // The activation as a clamp that lets NaN through (a median of three would not).
 __device__ __forceinline__ float clamp_act(float v, Act act) {
@@ -116,7 +117,9 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(Mx4Args a, long lon
 // ------------------------------------------------------------------------------------------
 // 16-bit tokens
 // ------------------------------------------------------------------------------------------
-// bf16 pieces of eight 16-bit inputs: fp16's 11 bits are two of them, exactly.
+// bf16 pieces of eight 16-bit inputs: fp16's 11 bits are two of them, exactly.  The first of an infinity is infinite;
+// what is left of it, inf - inf, is a NaN, on this card a negative one, and with it all its outputs would be NaN.  As a 16-bit
+// integer that lies above -256, and so becomes it (the second pieces are smaller): one instruction for two of them.
 template <typename T>
 struct XPieces {
     static constexpr int N = std::is_same<T, _Float16>::value ? 2 : 1;
@@ -134,7 +137,8 @@ __device__ __forceinline__ void x_pieces(u32x4 raw, u32x4* out) {
             out[0][i] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
             const float rl = v[2 * i] - __builtin_bit_cast(float, lo & 0xffff0000u);
             const float rh = v[2 * i + 1] - __builtin_bit_cast(float, hi & 0xffff0000u);
-            out[1][i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, rh), __builtin_bit_cast(uint32_t, rl), 0x07060302u);
+            const uint32_t rest = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, rh), __builtin_bit_cast(uint32_t, rl), 0x07060302u);
+            out[1][i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(u16x2, rest), u16x2{0xc380, 0xc380}));
         }
     }
 }
