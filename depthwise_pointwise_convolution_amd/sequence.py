@@ -567,7 +567,8 @@ class DraftVerifier:
     def kept(self, accepted, slots):
         """(cu, slots) of 2*requests sequences for a block's ``prompt`` over the verified rows, each request's
         last token and its drafts: the rows that stand move the state in the request's slot on, the rows
-        behind them belong to no slot.  (A caller's carry has 2*requests values.)"""
+        behind them belong to no slot.  (A caller's carry has 2*requests values.)  The states are bit for bit those
+        that the rows gave when they were verified if a request has at most 16, else within their rounding."""
         R, D = self.requests, self.drafts
         self._ints(accepted, R, "accepted", accepted.device)
         self._ints(slots, R, "slots", accepted.device)
