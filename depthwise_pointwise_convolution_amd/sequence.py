@@ -21,6 +21,7 @@ whole row of them at a time, in slots of their own, and the states then moved on
 Every call works on torch's current stream.  With ``stream`` (a torch stream or a raw handle) all of
 it, the projections and what it allocates among it, works on that stream instead, behind what the
 current stream holds at the call; whoever uses the results or the states on another stream waits for it.
+(What makes a layer's weights, and ``weight`` that shows them, take no ``stream``.)
 """
 from __future__ import annotations
 
@@ -564,11 +565,13 @@ class DraftVerifier:
         fcm_draft_verify(prob, target, draft, tokens, counts, uniform, ws, accepted, following)
         return accepted, following
 
-    def kept(self, accepted, slots):
+    def kept(self, accepted, slots, stream=None):
         """(cu, slots) of 2*requests sequences for a block's ``prompt`` over the verified rows, each request's
         last token and its drafts: the rows that stand move the state in the request's slot on, the rows
         behind them belong to no slot.  (A caller's carry has 2*requests values.)  The states are bit for bit those
         that the rows gave when they were verified if a request has at most 16, else within their rounding."""
+        if stream is not None:
+            return _on(stream, lambda: self.kept(accepted, slots), accepted, slots)
         R, D = self.requests, self.drafts
         self._ints(accepted, R, "accepted", accepted.device)
         self._ints(slots, R, "slots", accepted.device)
