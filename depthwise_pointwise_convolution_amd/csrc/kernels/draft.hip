@@ -274,8 +274,11 @@ __device__ __forceinline__ void join_splits(const Series& series, const Split* i
     *top = m;
 }
 
-// What a token counts for in the row that is drawn from, and its probability there.
+// What a token counts for in the row that is drawn from, and its probability there.  Where the draft's row is the
+// target's the difference has to be zero, or the token would be drawn from what roundings leave: the product is
+// rounded before it is taken off, not fused with the subtraction.
 __device__ __forceinline__ Sums draw_weight(const Series& series, const Row& row, float l, float d, int token, double inv, double ip, double iq) {
+#pragma clang fp contract(off)
     const double p = row.psum > 0.0 ? series.weight(l, row.ptop, inv) * ip : 0.0;
     double w = p;
     if (row.residual) {
