@@ -45,8 +45,10 @@ __host__ __device__ inline int row_splits(int vocab) {
 }
 __host__ __device__ inline int row_parts(int vocab) { return (vocab + kPart - 1) / kPart; }
 
-// exp(x) for x <= 0 in 64 bits: 2^n times the Taylor series of e^r to r^12, |r| <= log(2)/2, whose rest is below
-// 2^-52.  (At -750 it is zero, as far below.)  The coefficients are in scalar registers: as literals each of them
+// exp(x) for x <= 0 in 64 bits: Cody and Waite's reduction, x = n log(2) + r with log(2) in two parts, and 2^n times the
+// Taylor series of e^r to r^12, |r| <= log(2)/2, whose rest is below 2^-52.  The first part is log(2) cut to 40 bits behind the
+// point, so that its product with n, of up to 11 bits, is exact; the second is the rest, rounded.  (At -750 the value is zero,
+// as far below.)  The coefficients are in scalar registers: as literals each of them
 // would be moved to vector registers for each use, as many instructions again as the series has.
 struct Series {
     double c[11], log2e, high, low;
@@ -61,8 +63,8 @@ struct Series {
 #pragma unroll
         for (int i = 0; i < 11; ++i) c[i] = held(f[i]);
         log2e = held(1.4426950408889634);
-        high = held(-0.693147180369123816490);
-        low = held(-1.90821492927058770002e-10);
+        high = held(-0x1.62e42fefa2p-1);
+        low = held(-0x1.9ef35793c7673p-41);
     }
     __device__ __forceinline__ double exp_neg(double x) const {
         x = __builtin_fmax(x, -750.0);
