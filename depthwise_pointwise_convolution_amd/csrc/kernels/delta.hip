@@ -20,7 +20,7 @@
 // pieces, and the product of both seconds is left out: with the missing thirds 3 * 2^-16 of the sum of the products'
 // magnitudes at most, a tenth of what rounding the output to fp16 may take; with three, 4096 tokens of 16 heads took
 // 160 us instead of 150, 8192 of 32 401 instead of 394.  (Cut pieces, which round towards zero, cost the same and left
-// outputs 2^-15 too small.)  Quotients G_i / G_j are exponentials of differences of sums
+// sums of positive products 1.4e-5 too small on average.)  Quotients G_i / G_j are exponentials of differences of sums
 // held in 64 bits: in 32 the difference of two sums of a few hundred would be off by 2^-16.
 #include <float.h>
 #include <limits.h>

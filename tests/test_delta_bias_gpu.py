@@ -10,11 +10,11 @@ pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="n
 
 
 def test_outputs_of_positive_sums_are_not_too_small():
-    # Every product is positive, so that errors of one sign would add up.  The mean of 17000 roundings to fp16, each below
-    # 2^-11 of the value and as often up as down, has a standard deviation below 2^-11 / sqrt(3 * 17000) = 2.2e-6; that of
-    # the left out products, 3 * 2^-16 at most each and 64 of them a sum, is below 3.3e-6 for one output and averages out
-    # over the tokens.  Pieces cut towards zero leave 2^-15 = 3e-5 and more.
-    T, Hv, Dk, Dv = 130, 2, 64, 64
+    # Every product is positive, so that errors of one sign would add up.  The mean of 133000 roundings to fp16, each below
+    # 2^-11 of the value and as often up as down, has a standard deviation below 2^-11 / sqrt(3 * 133000) = 7.7e-7; that of
+    # the 150000 states' missing thirds, each below 2^-16, is below 2^-16 / sqrt(3 * 150000) = 2.3e-8.  Five of the first
+    # and the second are 4e-6.  Pieces cut towards zero miss half of 2^-15 of a state on average, 1e-5 and more.
+    T, Hv, Dk, Dv = 520, 4, 64, 64
     c = _inputs(11, "f16", T, 1, 1, Hv, Dk, Dv, 1)
     for n in ("q", "k", "v", "state"):
         c[n] = c[n].abs()
@@ -27,4 +27,5 @@ def test_outputs_of_positive_sums_are_not_too_small():
                   Dk ** -0.5, 1e-6)
     assert (y > 0).all()
     off = ((got.double().reshape(T, Hv, Dv) - y) / y).mean()
-    assert off.abs() <= 1.5e-5, float(off)
+    print("mean relative error", float(off))
+    assert off.abs() <= 4e-6, float(off)
