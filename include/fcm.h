@@ -581,13 +581,14 @@ fcm_status fcm_mx4_dequantize(const fcm_mx4_problem* prob, const void* q, const 
 
 /* Pointwise layer y[m][k] = act(bias[k] + sum_c W[k][c] * x[m][c]) with W in codes: q [K][C/2], scales
  * [K][C/32], bias [K] fp32 or NULL.  x: [M][C] in the storage type; for a few tokens (the weights are
- * read and converted once for every 32 of them).  Products of a block's values are exact and summed in fp32.  x and q need
- * 16-byte alignment and ldx a multiple of 8. */
+ * read and converted once for every 32 of them).  Products of a block's values are exact and summed in fp32.  A weight of
+ * 2^128 and above (a large code with the scale 253 or 254, which fcm_mx4_quantize never gives) counts as infinite; its
+ * outputs are infinite or NaN.  x and q need 16-byte alignment and ldx a multiple of 8. */
 fcm_status fcm_mx4_fwd(const fcm_mx4_problem* prob, const void* x, const void* q, const uint8_t* scales,
                        const float* bias, void* y, void* stream);
 
 /* The same with x in codes too, xq [M][C/2] and xscales [M][C/32], on the scaled matrix instructions,
- * for any number of tokens.  xq and q need 16-byte alignment; ldx is not used. */
+ * for any number of tokens, and any weight.  xq and q need 16-byte alignment; ldx is not used. */
 fcm_status fcm_mx4x4_fwd(const fcm_mx4_problem* prob, const void* xq, const uint8_t* xscales,
                          const void* q, const uint8_t* scales, const float* bias, void* y,
                          void* stream);
