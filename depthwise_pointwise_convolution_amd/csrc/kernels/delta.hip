@@ -901,7 +901,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slic
 // y written without a place in the caches, which leaves it to the outputs (with one: 61 us).  Outputs in the storage type would
 // be 67 MB less to read, but a second rounding, and infinite above fp16's largest number though the norm brings them to 1.
 constexpr int kNormRows = 4;
-template <typename T, bool WIDE>
+template <typename T, bool WIDE, bool ASK>
 __global__ __launch_bounds__(256) void delta_norm_kernel(DeltaArgs a, int slices, int width) {
     constexpr int VE = Vec<T>::N;
     const int x = threadIdx.x & (width - 1), groups = 256 / width;
@@ -920,6 +920,7 @@ __global__ __launch_bounds__(256) void delta_norm_kernel(DeltaArgs a, int slices
         const long long t = id / (uint32_t)a.Hv;
         const int h = id - (uint32_t)t * a.Hv;
         live[r] = t >= from && t < to;
+        if (ASK) live[r] = live[r] && !(a.squares[(long long)id * slices] < 0.0f);
         if (!live[r]) continue;
         y[r] = (T*)a.y + t * a.ldy + (long long)h * a.Dv;
         o[r] = sizeof(T) < 4 ? a.outs + (long long)id * a.Dv : (const float*)y[r];
@@ -1172,10 +1173,15 @@ int run(DeltaArgs a, hipStream_t s) {
     const int rows = 256 / width * kNormRows;
     const int grid = (int)(((long long)a.tokens * a.Hv + rows - 1) / rows);
     const bool wide = a.Dv % VE == 0 && rows16(a.y, a.ldy, sizeof(T)) && (!a.z || rows16(a.z, a.ldz, sizeof(T)));
-    if (wide)
-        delta_norm_kernel<T, true><<<grid, 256, 0, s>>>(a, slices, width);
+    // Where most sequences are likely short it first asks whose the rows are: 32 sequences of 5 tokens take 57 us with the kernels
+    // before it instead of 60, as rows that are done take no place in the caches; of 8192 tokens of 11 sequences it would
+    // take 57 us instead of 55, of one of 4096 17 instead of 16.
+    if (!wide)
+        delta_norm_kernel<T, false, false><<<grid, 256, 0, s>>>(a, slices, width);
+    else if (a.shortest > 0 && a.tokens < 2ll * kShort * a.seqs)
+        delta_norm_kernel<T, true, true><<<grid, 256, 0, s>>>(a, slices, width);
     else
-        delta_norm_kernel<T, false><<<grid, 256, 0, s>>>(a, slices, width);
+        delta_norm_kernel<T, true, false><<<grid, 256, 0, s>>>(a, slices, width);
     return (int)hipGetLastError();
 }
 

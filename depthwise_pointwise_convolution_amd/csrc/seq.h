@@ -71,10 +71,10 @@ struct DeltaArgs {
     int Hk, Hv, Dk, Dv, tokens, seqs, nslots, qk_norm, softplus;
     // set by the launcher
     long long places;  // for chunks, in the workspace
-    float* outs;       // before the norm, of 16-bit types
     float* squares;
     int wide_q, wide_k, wide_v, wide_z, wide_y, wide_state;  // alignment for vectors
     int shortest;  // sequences of up to so many tokens are another kernel's
+    float* outs;   // before the norm, of 16-bit types
 };
 int launch_delta_fwd(DeltaArgs a, int dtype, void* stream);
 int launch_delta_step(const DeltaArgs& a, int dtype, void* stream);

@@ -45,7 +45,8 @@ def test_norm_of_32_bit_outputs(dtype, values, states, eps, lens, Hk, Hv, Dk, Dv
     assert (d <= ytol).all(), (float((d / ytol).max()), int((d > ytol).sum()))
 
 
-def test_many_sequences_with_a_norm():
+@pytest.mark.parametrize("pad", [0, 1])
+def test_many_sequences_with_a_norm(pad):
     # two tiles of columns a slice
     lens, Hk, Hv, Dk, Dv = [17, 30, 2, 66] * 32, 2, 4, 64, 48
     T, B = sum(lens), len(lens)
@@ -53,5 +54,5 @@ def test_many_sequences_with_a_norm():
     c["state"] *= 1e6
     ends = torch.tensor([0] + lens).cumsum(0).tolist()
     y, ytol = _want("f16", c, list(zip(ends, ends[1:])), list(range(B)), [1] * B, Dk, Dv, 1e-6)
-    got, _, _ = _call(c, "f16", lens, list(range(B)), [1] * B, Hk, Hv, Dk, Dv, {}, pad=1)
+    got, _, _ = _call(c, "f16", lens, list(range(B)), [1] * B, Hk, Hv, Dk, Dv, {}, pad=pad)
     assert ((got.double().reshape(T, Hv, Dv) - y).abs() <= ytol).all()
