@@ -171,7 +171,7 @@ __device__ __forceinline__ void st_operand(char* p, u32x4 v) {
 }
 
 // One workgroup per chunk and key head.  What is written bounds it: for 8192 tokens of 16 key heads and 32 value heads of
-// 128 channels 225 MB (and 100 MB read) in 95 us, 3.4 TB/s; where there are few workgroups it is the latency of one, 26 us.
+// 128 channels 225 MB (and 100 MB read) in 85 us, 3.8 TB/s; where there are few workgroups it is the latency of one, 26 us.
 // The value heads' decays are summed four heads at a time, a wave each, while the rows are under way.
 template <typename T, int NKB>
 __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
@@ -561,7 +561,8 @@ int long_sequences(int seqs, int tokens, int shortest) {
 // chunk is loaded as soon as this one is done with the registers.
 //
 // The chain's latency bounds it: 16 heads of one sequence take 1.6 us a chunk (2.9 with all of it on four waves), 8192
-// tokens of 32 heads of 128 channels 235 us, 3.6 us a chunk of one workgroup a CU, where its products are 0.75 us.
+// tokens of 32 heads of 128 channels 250 us, 3.8 us a chunk of one workgroup a CU, where its products are 0.75 us: the
+// matrix units are busy in 21% of its cycles, LDS in 24%, and its waves wait for results in 46% of theirs.
 template <typename T, int NKB, int NT>
 __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slices) {
     constexpr int PI = Pieces<T>::IN, PQ = Pieces<T>::OUT, KW = (NKB + 3) / 4;
@@ -897,7 +898,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, int slic
 // The output's norm and gate: the second kernel left the outputs in 32 bits (in the workspace, or in y where that has
 // them) and its slices their sums of squares, a negative one the short sequences' kernel, which has done it all.  A group
 // of `width` lanes has kNormRows rows of heads, one after the other in memory, whose loads are all under way before the
-// first is used.  HBM bounds it: 8192 tokens of 32 heads of 128 channels in bf16, 268 MB, in 56 us, 4.8 TB/s.  z is read and
+// first is used.  HBM bounds it: 8192 tokens of 32 heads of 128 channels in bf16, 268 MB, in 55 us, 4.9 TB/s.  z is read and
 // y written without a place in the caches, which leaves it to the outputs (with one: 61 us).  Outputs in the storage type would
 // be 67 MB less to read, but a second rounding, and infinite above fp16's largest number though the norm brings them to 1.
 constexpr int kNormRows = 4;

@@ -23,7 +23,7 @@ __device__ __forceinline__ float clamp_act(float v, Act act) {
 __device__ __forceinline__ float scale_float(uint32_t code) { return __builtin_bit_cast(float, code << 23); }
 
 // ------------------------------------------------------------------------------------------
-// quantisation: eight channels a lane, four lanes a block.  HBM bounds it: 8192 x 4096 bf16, 85 MB, in 18 us, 4.8 TB/s
+// quantisation: eight channels a lane, four lanes a block.  HBM bounds it: 8192 x 4096 bf16, 85 MB, in 19 us, 4.5 TB/s
 // ------------------------------------------------------------------------------------------
 constexpr int kPer = 4;  // pieces of eight channels of a thread
 
@@ -201,7 +201,10 @@ struct StepScales {
 // block, in the same order from both sides.
 //
 // HBM bounds few tokens, and the conversions in turns with it more of them: 4096 channels -> 65536, 143 MB of codes,
-// with 1 token 32 us (4.5 TB/s), 8 tokens 38, 16 tokens 40, 32 tokens 53; 2048 -> 8192 with one token 4.1, the launch.
+// with 1 token 32 us (4.5 TB/s), 4 tokens 34, 8 tokens 38 (3.8 TB/s), 16 tokens 40, 32 tokens 55; in fp16, whose tokens are
+// two pieces, 34, 36, 39, 40 and 77; 2048 -> 8192 with one token 4.1, the launch.  Prompts it reads the weights for again and
+// again: 4096 -> 8192 takes 1024 tokens 156 us and 8192 tokens 1153, with the tokens quantised for the kernels below 42 and
+// 207.
 template <typename T, int NI, int MT, int RT, int NW>
 __global__ __launch_bounds__(64 * NW) void mx4_kernel(Mx4Args a) {
     constexpr int XI = MT * NI, TOKENS = 4 * XI, XP = XPieces<T>::N;
@@ -599,9 +602,11 @@ __device__ __forceinline__ void order() {
 // step goes to LDS and the one after is loaded.  The barrier between the third and the fourth says that all waves have
 // read this step and stored the next, whose first operands are read in the fourth.
 //
-// The power that the products draw bounds it, at 1.9 GHz: 8192 tokens, 4096 -> 8192 channels, take 182 us (3.0 PFLOP/s;
-// 4.4 inside a tile, the rest are the starts and ends of the four tiles that each CU has).  With eight waves and a
-// 128-channel step it was 230, with two workgroups of 128 x 256 a CU 224.
+// 8192 tokens, 4096 -> 8192 channels, take 185 us (3.0 PFLOP/s; 4.4 inside a tile, the rest are the starts and ends of the
+// four tiles that each CU has).  No unit is full: at the 1.9 GHz that the card holds here the matrix units, whose
+// instruction alone makes 8.1 PFLOP/s, are busy in 37% of the cycles (55% inside a tile), LDS in 39% and 15% more for banks
+// asked twice, and the one wave of a SIMD waits for results in 22%.  What bounds it is that one wave, which has to issue all of
+// it one after the other.  With eight waves and a 128-channel step it was 230, with two workgroups of 128 x 256 a CU 224.
 template <typename T>
 __global__ __launch_bounds__(256, 1) void mx4x4_large_kernel(Mx4Args a, int mtiles, int ktiles) {
     constexpr int TILE = 256, ROWS = 2 * TILE, R = 4, LOADS = 16, SPAN = 4;

@@ -208,7 +208,9 @@ class MX4Linear:
     """y = act(x W^T + bias) with W in microscaled 4-bit floating point: q [K, C/2] and scales [K, C/32],
     uint8 (see :func:`quantize_mx4`), bias [K] float32 or None; activations of `dtype`.  With
     `quantize_input` x goes into the same codes first and the product runs on the scaled matrix
-    instructions, for prompts of any length; without, it is meant for a few tokens."""
+    instructions, for prompts of any length; without, it is meant for a few tokens (the weights are read
+    and converted again for every 32: 4096 -> 8192 channels take 13 us for 64 tokens, 1153 for 8192, with
+    `quantize_input` 12 and 207)."""
 
     def __init__(self, q, scales, bias=None, act: str = "none", dtype: torch.dtype = torch.bfloat16,
                  quantize_input: bool = False):
