@@ -501,8 +501,10 @@ fcm_status fcm_scan_step(const fcm_scan_problem* prob, const void* x, const void
  *   o[j] = sum_i q'[i] * S[i][j]
  *   y[t][h][j] = o[j] * (norm ? norm[j] / sqrt(mean of o's squares + eps) : 1) * (z ? z * sigmoid(z) : 1)
  * A <= 0 and beta * |k'|^2 < 2 keep the recurrence bounded.  A step d of zero keeps the state, whatever
- * A.  Sequences of up to 16 tokens give what the single-token call gives for each of them, bit for bit.
- * Longer ones are computed in chunks of 64 tokens, with other sums: a value that is not finite (in 32 bits: below 2^128 - 2^119) makes the outputs of its
+ * A.  Squares and their sums are fp32: rows whose length passes 1e19 are beyond them.
+ * A sequence of up to 16 tokens gives what the single-token call gives for each of them, bit for bit (if it is its call's
+ * only one: where the call has no more than 16 rows).  Longer ones are computed in chunks of 64 tokens, with other sums,
+ * and a value that is not finite (in 32 bits: below 2^128 - 2^119) makes the outputs of its
  * own head's whole chunk, and the head's outputs and state after it, possibly not finite; other heads and
  * sequences are as they would be without it. */
 typedef struct {

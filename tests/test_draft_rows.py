@@ -72,3 +72,16 @@ def test_sixteen_tokens_are_sixteen_steps(dtype, B, Hk, Hv, Dk, Dv, norm):
         got.append((y, s))
     for y, s in got[1:]:
         assert torch.equal(y, got[0][0]) and torch.equal(s, got[0][1])
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_a_short_sequence_alone_among_padding(dtype):
+    # goes in a chunk: within its bound, and the rows behind it are left
+    from recurrent_oracle import delta
+    from test_delta_gpu import _call, _check, _inputs
+    c = _inputs(3, dtype, 40, 1, 1, 2, 64, 48, 1)
+    got, pool, spans = _call(c, dtype, [10], [0], [1], 1, 2, 64, 48, {})
+    want = delta(dtype, c["q"], c["k"], c["v"], c["a"], c["b"], c["A"], c["dt_bias"], c["norm"], c["z"], spans, [0], [1],
+                 c["state"], 64 ** -0.5, 1e-6)
+    _check(got, pool, want, 40, 2, 48, dtype)
