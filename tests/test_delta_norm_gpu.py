@@ -56,3 +56,51 @@ def test_many_sequences_with_a_norm(pad):
     y, ytol = _want("f16", c, list(zip(ends, ends[1:])), list(range(B)), [1] * B, Dk, Dv, 1e-6)
     got, _, _ = _call(c, "f16", lens, list(range(B)), [1] * B, Hk, Hv, Dk, Dv, {}, pad=pad)
     assert ((got.double().reshape(T, Hv, Dv) - y).abs() <= ytol).all()
+
+
+def test_outputs_behind_the_2_to_the_31st():
+    # the last sequence's rows, whose 32-bit outputs lie behind 2^31 elements, are bit for bit those of it alone
+    import depthwise_pointwise_convolution_amd as F
+    Hk, Hv, Dk, Dv, last = 1, 64, 32, 256, 100
+    T = 2 ** 31 // (Hv * Dv) + 2 * last
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = {n: torch.randn(T, w, device="cuda", generator=g, dtype=torch.bfloat16)
+         for n, w in (("q", Hk * Dk), ("k", Hk * Dk), ("v", Hv * Dv), ("a", Hv), ("b", Hv), ("z", Hv * Dv))}
+    A, norm = -torch.ones(Hv, device="cuda"), torch.ones(Dv, device="cuda")
+    got = []
+    for rows in (T, last):
+        d = {n: v[-rows:] for n, v in x.items()}
+        p = F.delta_problem("bf16", Hk, Hv, Dk, Dv, tokens=rows, seqs=2, slots=2)
+        ws = torch.empty(F.fcm_delta_workspace(p), dtype=torch.uint8, device="cuda")
+        state = torch.ones(2, Hv, Dk, Dv, device="cuda")
+        y = torch.empty(rows, Hv * Dv, dtype=torch.bfloat16, device="cuda")
+        cu = torch.tensor([0, rows - last, rows], dtype=torch.int32).cuda()
+        F.fcm_delta_fwd(p, d["q"], d["k"], d["v"], d["a"], d["b"], A, None, norm, d["z"], cu, None,
+                        torch.ones(2, dtype=torch.int32).cuda(), state, ws, y)
+        torch.cuda.synchronize()
+        got.append((y[-last:].clone(), state[1].clone()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert torch.isfinite(got[0][0].float()).all()
+
+
+def test_two_at_once():
+    # two prompts' calls on streams of their own, each with its workspace, give what they give one after the other
+    import depthwise_pointwise_convolution_amd as F
+    Hk, Hv, Dk, Dv, lens = 2, 4, 64, 64, [300, 5, 200]
+    T, B = sum(lens), len(lens)
+    cu = torch.tensor([0, 300, 305, 505], dtype=torch.int32).cuda()
+    p = F.delta_problem("f16", Hk, Hv, Dk, Dv, tokens=T, seqs=B, slots=B)
+    cases = [{n: t.cuda() for n, t in _inputs(seed, "f16", T, B, Hk, Hv, Dk, Dv, B).items()} for seed in (1, 2)]
+    out = [[(torch.empty(T, Hv * Dv, dtype=torch.float16, device="cuda"), c["state"].clone(),
+             torch.empty(F.fcm_delta_workspace(p), dtype=torch.uint8, device="cuda")) for c in cases] for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for together in (False, True):
+        for c, (y, state, ws), s in zip(cases, out[together], streams):
+            F.fcm_delta_fwd(p, c["q"], c["k"], c["v"], c["a"], c["b"], c["A"], c["dt_bias"], c["norm"], c["z"], cu, None,
+                            None, state, ws, y, stream=s.cuda_stream if together else None)
+            if not together:
+                torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    for (y, state, _), (z, other, _) in zip(*out):
+        assert torch.equal(y, z) and torch.equal(state, other)
